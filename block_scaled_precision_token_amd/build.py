@@ -17,7 +17,7 @@ LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libbsp.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 
-SOURCES = ["bsp_capi.cpp", "bsp_quant.hip", "bsp_gemm.hip"]
+SOURCES = ["bsp_capi.cpp", "bsp_quant.hip", "bsp_gemm.hip", "bsp_route.hip", "bsp_checkpoint.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-ffp-contract=off", "-fno-fast-math", "-fvisibility=hidden",

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include "bsp_internal.hpp"
+#include "bsp_moe.hpp"
 
 #define BSP_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -373,4 +374,114 @@ BSP_EXPORT bsp_status bsp_swiglu_quantize(const void *h13, int in_dtype, int64_t
     return hip_status(bsp::launch_swiglu(h13, in_dtype, R, I, h_out, fmt, (flags & BSP_NVFP4_46) != 0,
                                          fmt >= 0 ? codes : nullptr, fmt >= 0 ? scales : nullptr,
                                          fmt == BSP_FMT_NVFP4 ? outer : nullptr, as_stream(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// routing, SwiGLU checkpoint, combine
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// Sizes that bsp_moe_route and its backward share: the kernels keep expert
+// ids, tokens and grouped rows in 32 bits.
+inline bsp_status route_shape(int64_t T, int64_t E, int64_t ld, int64_t k, int64_t shared) {
+    if (T <= 0 || E < 1 || E > 1024 || ld < E || k < 1 || k > 32 || k > E || shared < 0 || shared > 64)
+        return BSP_ERR_SHAPE;
+    const int64_t lim31 = (1ll << 31) - 1;
+    if (T > lim31 / (k + shared) || ld > (1ll << 32)) return BSP_ERR_SHAPE;
+    return BSP_OK;
+}
+
+inline bool known_dtype(int d) { return d == BSP_DTYPE_F32 || d == BSP_DTYPE_BF16; }
+
+}  // namespace
+
+BSP_EXPORT size_t bsp_moe_route_workspace_size(int64_t T, int64_t E, int64_t shared) {
+    if (route_shape(T, E, E, 1, shared) != BSP_OK) return 0;
+    return (size_t)bsp::route_workspace_bytes(T, E, shared);
+}
+
+BSP_EXPORT bsp_status bsp_moe_route(const void *logits, int dtype, int64_t T, int64_t E, int64_t ldl,
+                                    const uint8_t *token_mask, int64_t k, int64_t shared, int32_t *experts,
+                                    float *weights, int32_t *counts, int64_t *group_offsets, int32_t *src,
+                                    int32_t *pos, float *row_weights, float *prob_sum, float *loss, uint32_t flags,
+                                    void *workspace, size_t ws_bytes, void *stream) {
+    if (!logits || !experts || !weights || !counts || !group_offsets || !src || !pos || !row_weights)
+        return BSP_ERR_INVALID_ARG;
+    if ((prob_sum == nullptr) != (loss == nullptr)) return BSP_ERR_INVALID_ARG;
+    if (!known_dtype(dtype) || (flags & ~BSP_ROUTE_NORM)) return BSP_ERR_INVALID_ARG;
+    const bsp_status shape = route_shape(T, E, ldl, k, shared);
+    if (shape != BSP_OK) return shape;
+    const size_t need = bsp_moe_route_workspace_size(T, E, shared);
+    if (need > 0 && (!workspace || ws_bytes < need)) return BSP_ERR_WORKSPACE;
+    if (!aligned16(logits) || !aligned16_or_null(token_mask) || !aligned16(experts) || !aligned16(weights) ||
+        !aligned16(counts) || !aligned16(group_offsets) || !aligned16(src) || !aligned16(pos) ||
+        !aligned16(row_weights) || !aligned16_or_null(prob_sum) || !aligned16_or_null(loss) ||
+        !aligned16_or_null(workspace))
+        return BSP_ERR_ALIGNMENT;
+    return hip_status(bsp::launch_route(logits, dtype, T, E, ldl, token_mask, k, shared, experts, weights, counts,
+                                        group_offsets, src, pos, row_weights, prob_sum, loss,
+                                        (flags & BSP_ROUTE_NORM) != 0, workspace, as_stream(stream)));
+}
+
+BSP_EXPORT bsp_status bsp_moe_route_backward(const void *logits, int dtype, int64_t T, int64_t E, int64_t ldl,
+                                             const uint8_t *token_mask, int64_t k, int64_t shared,
+                                             const int32_t *experts, const int32_t *pos, const int32_t *counts,
+                                             const float *d_weights, const float *d_loss, void *d_logits,
+                                             int64_t ldd, uint32_t flags, void *stream) {
+    if (!logits || !experts || !pos || !counts || !d_logits || (!d_weights && !d_loss)) return BSP_ERR_INVALID_ARG;
+    if (!known_dtype(dtype) || (flags & ~BSP_ROUTE_NORM)) return BSP_ERR_INVALID_ARG;
+    const bsp_status shape = route_shape(T, E, ldl < ldd ? ldl : ldd, k, shared);
+    if (shape != BSP_OK) return shape;
+    if ((ldl > ldd ? ldl : ldd) > (1ll << 32)) return BSP_ERR_SHAPE;
+    if (!aligned16(logits) || !aligned16_or_null(token_mask) || !aligned16(experts) || !aligned16(pos) ||
+        !aligned16(counts) || !aligned16_or_null(d_weights) || !aligned16_or_null(d_loss) || !aligned16(d_logits))
+        return BSP_ERR_ALIGNMENT;
+    return hip_status(bsp::launch_route_backward(logits, dtype, T, E, ldl, token_mask, k, shared, experts, pos, counts,
+                                                 d_weights, d_loss, d_logits, ldd, (flags & BSP_ROUTE_NORM) != 0,
+                                                 as_stream(stream)));
+}
+
+BSP_EXPORT bsp_status bsp_swiglu_checkpoint(const void *h13, int in_dtype, int64_t R, int64_t I,
+                                            const float *row_weights, const int64_t *n_rows, uint16_t *h_out,
+                                            uint8_t *codes, uint8_t *scales, uint8_t *ckpt_codes,
+                                            uint8_t *ckpt_scales, void *stream) {
+    if (!h13 || !ckpt_codes || !ckpt_scales || (!h_out && !codes)) return BSP_ERR_INVALID_ARG;
+    if ((codes == nullptr) != (scales == nullptr)) return BSP_ERR_INVALID_ARG;
+    if (!known_dtype(in_dtype)) return BSP_ERR_INVALID_ARG;
+    if (R <= 0 || R >= (1ll << 31) || I <= 0 || I % 32 || I > (1ll << 24)) return BSP_ERR_SHAPE;
+    if (!aligned16(h13) || !aligned16_or_null(row_weights) || !aligned16_or_null(h_out) ||
+        !aligned16_or_null(codes) || !aligned16_or_null(scales) || !aligned16(ckpt_codes) || !aligned16(ckpt_scales) ||
+        (reinterpret_cast<uintptr_t>(n_rows) & 7u))
+        return BSP_ERR_ALIGNMENT;
+    return hip_status(bsp::launch_swiglu_checkpoint(h13, in_dtype, R, I, row_weights, n_rows, h_out, codes, scales,
+                                                    ckpt_codes, ckpt_scales, as_stream(stream)));
+}
+
+BSP_EXPORT bsp_status bsp_swiglu_checkpoint_backward(const void *dh, int dtype, int64_t R, int64_t I,
+                                                     const uint8_t *ckpt_codes, const uint8_t *ckpt_scales,
+                                                     const float *row_weights, const int64_t *n_rows, void *dh13,
+                                                     uint16_t *h_out, float *d_row_weights, void *stream) {
+    if (!dh || !ckpt_codes || !ckpt_scales || !dh13 || !known_dtype(dtype)) return BSP_ERR_INVALID_ARG;
+    if (R <= 0 || R >= (1ll << 31) || I <= 0 || I % 32 || I > (1ll << 24)) return BSP_ERR_SHAPE;
+    if (!aligned16(dh) || !aligned16(ckpt_codes) || !aligned16(ckpt_scales) || !aligned16_or_null(row_weights) ||
+        !aligned16(dh13) || !aligned16_or_null(h_out) || !aligned16_or_null(d_row_weights) ||
+        (reinterpret_cast<uintptr_t>(n_rows) & 7u))
+        return BSP_ERR_ALIGNMENT;
+    return hip_status(bsp::launch_swiglu_checkpoint_backward(dh, dtype, R, I, ckpt_codes, ckpt_scales, row_weights,
+                                                             n_rows, dh13, h_out, d_row_weights, as_stream(stream)));
+}
+
+BSP_EXPORT bsp_status bsp_moe_combine(const void *y, int in_dtype, int64_t rows, int64_t H, int64_t ldy,
+                                      const int32_t *pos, const float *weights, int64_t T, int64_t kk, void *out,
+                                      int out_dtype, int64_t ldo, void *stream) {
+    if (!y || !pos || !out || !known_dtype(in_dtype) || !known_dtype(out_dtype)) return BSP_ERR_INVALID_ARG;
+    if (rows <= 0 || T <= 0 || H <= 0 || H % 8 || ldy < H || ldo < H || kk < 1 || kk > 128) return BSP_ERR_SHAPE;
+    const int64_t lim31 = (1ll << 31) - 1;
+    if (T > lim31 / kk || rows > lim31 || ldy > (1ll << 32) || ldo > (1ll << 32)) return BSP_ERR_SHAPE;
+    if (H > (1ll << 24) || T > (1ll << 38) / H) return BSP_ERR_SHAPE;   // grid size
+    if (ldy % 8 || ldo % 8 || !aligned16(y) || !aligned16(pos) || !aligned16_or_null(weights) || !aligned16(out))
+        return BSP_ERR_ALIGNMENT;
+    return hip_status(bsp::launch_combine(y, in_dtype, rows, H, ldy, pos, weights, T, kk, out, out_dtype, ldo,
+                                          as_stream(stream)));
 }

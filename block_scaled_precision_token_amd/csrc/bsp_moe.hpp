@@ -1,0 +1,66 @@
+// bsp_moe.hpp -- launch entry points of the routing, SwiGLU-checkpoint and
+// combine kernels, shared between their files and the C ABI shim (which
+// validates the arguments first), and device helpers those kernels share.
+#pragma once
+
+#include "bsp_device.hpp"
+#include "bsp_internal.hpp"
+
+namespace bsp {
+
+int64_t route_workspace_bytes(int64_t T, int64_t E, int64_t shared);
+hipError_t launch_route(const void *logits, int dtype, int64_t T, int64_t E, int64_t ldl, const uint8_t *mask,
+                        int64_t k, int64_t shared, int32_t *experts, float *weights, int32_t *counts, int64_t *off,
+                        int32_t *src, int32_t *pos, float *row_weights, float *prob_sum, float *loss, bool norm,
+                        void *workspace, hipStream_t s);
+hipError_t launch_route_backward(const void *logits, int dtype, int64_t T, int64_t E, int64_t ldl,
+                                 const uint8_t *mask, int64_t k, int64_t shared, const int32_t *experts,
+                                 const int32_t *pos, const int32_t *counts, const float *d_weights,
+                                 const float *d_loss, void *d_logits, int64_t ldd, bool norm, hipStream_t s);
+hipError_t launch_combine(const void *y, int in_dtype, int64_t rows, int64_t H, int64_t ldy, const int32_t *pos,
+                          const float *weights, int64_t T, int64_t kk, void *out, int out_dtype, int64_t ldo,
+                          hipStream_t s);
+hipError_t launch_swiglu_checkpoint(const void *h13, int in_dtype, int64_t R, int64_t I, const float *row_weights,
+                                    const int64_t *n_rows, uint16_t *h_out, uint8_t *codes, uint8_t *scales,
+                                    uint8_t *ckpt_codes, uint8_t *ckpt_scales, hipStream_t s);
+hipError_t launch_swiglu_checkpoint_backward(const void *dh, int dtype, int64_t R, int64_t I,
+                                             const uint8_t *ckpt_codes, const uint8_t *ckpt_scales,
+                                             const float *row_weights, const int64_t *n_rows, void *dh13,
+                                             uint16_t *h_out, float *d_row_weights, hipStream_t s);
+
+// ---- device helpers shared by the kernels of these entry points ----
+
+// Sum over the 64 lanes, the same bits on every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+// Eight consecutive values (16-byte aligned) as f32, and back (bf16: nearest even).
+__device__ __forceinline__ void ld8(const float *p, float (&v)[8]) {
+    const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+}
+__device__ __forceinline__ void ld8(const uint16_t *p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+__device__ __forceinline__ void st8(float *p, const float (&v)[8]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void st8(uint16_t *p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = f32_to_bf16(v[2 * i]) | (f32_to_bf16(v[2 * i + 1]) << 16);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace bsp

@@ -26,6 +26,7 @@ GEMM_DGRAD = 1
 GEMM_WGRAD = 2
 NVFP4_46 = 0x1
 SR = 0x2
+ROUTE_NORM = 0x4
 
 STATUS = {0: "BSP_OK", 1: "BSP_ERR_INVALID_ARG", 2: "BSP_ERR_SHAPE", 3: "BSP_ERR_ALIGNMENT",
           4: "BSP_ERR_UNSUPPORTED", 5: "BSP_ERR_WORKSPACE", 6: "BSP_ERR_HIP", 7: "BSP_ERR_SCRATCH_LIMIT"}
@@ -38,7 +39,8 @@ EXPORTED = [
     "bsp_moe_grouped_gemm_bf16", "bsp_gemm_bf16_workspace_size", "bsp_requant_transpose_sr_batched",
     "bsp_requant_batched_workspace_size", "bsp_requant_transpose_sr_grouped", "bsp_quantize_nvfp4_rht",
     "bsp_quantize_nvfp4_2d", "bsp_moe_grouped_gemm_blockscaled_tiled", "bsp_moe_grouped_gemm_bf16_tiled",
-    "bsp_moe_grouped_gemm_blockscaled_noalloc",
+    "bsp_moe_grouped_gemm_blockscaled_noalloc", "bsp_moe_route", "bsp_moe_route_workspace_size",
+    "bsp_moe_route_backward", "bsp_swiglu_checkpoint", "bsp_swiglu_checkpoint_backward", "bsp_moe_combine",
 ]
 
 
@@ -91,11 +93,20 @@ def _declare(lib):
     lib.bsp_requant_workspace_size.restype = SZ
     lib.bsp_gemm_workspace_size.argtypes = [INT, INT, I64, I64, I64, I64]
     lib.bsp_gemm_workspace_size.restype = SZ
+    lib.bsp_moe_route.argtypes = [P, INT, I64, I64, I64, P, I64, I64, P, P, P, P, P, P, P, P, P, U32, P, SZ, P]
+    lib.bsp_moe_route_workspace_size.argtypes = [I64, I64, I64]
+    lib.bsp_moe_route_workspace_size.restype = SZ
+    lib.bsp_moe_route_backward.argtypes = [P, INT, I64, I64, I64, P, I64, I64, P, P, P, P, P, P, I64, U32, P]
+    lib.bsp_swiglu_checkpoint.argtypes = [P, INT, I64, I64, P, P, P, P, P, P, P, P]
+    lib.bsp_swiglu_checkpoint_backward.argtypes = [P, INT, I64, I64, P, P, P, P, P, P, P, P]
+    lib.bsp_moe_combine.argtypes = [P, INT, I64, I64, I64, P, P, I64, I64, P, INT, I64, P]
     for name in ("bsp_quantize_nvfp4_per_token", "bsp_quantize_mxfp8", "bsp_dequantize", "bsp_requant_transpose_sr",
                  "bsp_moe_grouped_gemm_blockscaled", "bsp_swiglu_quantize", "bsp_nvfp4_sizes", "bsp_mxfp8_sizes",
                  "bsp_moe_grouped_gemm_bf16", "bsp_requant_transpose_sr_batched", "bsp_requant_transpose_sr_grouped",
                  "bsp_quantize_nvfp4_rht", "bsp_quantize_nvfp4_2d", "bsp_moe_grouped_gemm_blockscaled_tiled",
-                 "bsp_moe_grouped_gemm_bf16_tiled", "bsp_moe_grouped_gemm_blockscaled_noalloc"):
+                 "bsp_moe_grouped_gemm_bf16_tiled", "bsp_moe_grouped_gemm_blockscaled_noalloc", "bsp_moe_route",
+                 "bsp_moe_route_backward", "bsp_swiglu_checkpoint", "bsp_swiglu_checkpoint_backward",
+                 "bsp_moe_combine"):
         getattr(lib, name).restype = INT
 
 
@@ -134,7 +145,7 @@ def _stream(device):
 # can be exercised without a GPU; nothing is launched on that path.
 DEVICE_TYPE = "cuda"
 
-_DT = {"u8": torch.uint8, "bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "i64": torch.int64}
+_DT = {"u8": torch.uint8, "bool": torch.bool, "bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "i64": torch.int64}
 
 
 def _need_cuda(t, name):
@@ -149,8 +160,8 @@ def _rowmajor(t, name):
 
 def _arg(t, name, dev, dtype, numel=None, optional=False, contiguous=True):
     """Check one tensor argument before its pointer goes to the library: a
-    device tensor on `dev` of the given dtype ("u8", "bf16", "f32", "i32",
-    "i64" or a tuple of them), contiguous, with at least `numel` elements.
+    device tensor on `dev` of the given dtype ("u8", "bool", "bf16", "f32",
+    "i32", "i64" or a tuple of them), contiguous, with at least `numel` elements.
     Raises ValueError; returns t."""
     if t is None:
         if optional:
@@ -619,3 +630,208 @@ def swiglu_quantize(h13: torch.Tensor, fmt: int = -1, mode46: bool = False, retu
                                         NVFP4_46 if mode46 else 0, _stream(dev))
     _check(st, "bsp_swiglu_quantize")
     return h, codes, scales, outer
+
+
+# ---------------------------------------------------------------------------
+# routing, SwiGLU checkpoint, combine
+# ---------------------------------------------------------------------------
+
+def _matrix_arg(t, name, dev=None, dtype=None):
+    """A 2-D f32 or bf16 tensor with unit column stride; returns its C dtype."""
+    _need_cuda(t, name)
+    _rowmajor(t, name)
+    if t.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must have dtype {dtype or 'f32 or bf16'}, not {t.dtype}")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return DTYPE_BF16 if t.dtype == torch.bfloat16 else DTYPE_F32
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor; torch leaves a single row's stride free."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def moe_route_workspace_size(T: int, E: int, shared: int = 0) -> int:
+    return int(_lib_raw().bsp_moe_route_workspace_size(T, E, shared))
+
+
+def moe_route(logits: torch.Tensor, k: int, norm: bool = True, shared: int = 0, token_mask=None, aux: bool = False,
+              out=None, workspace=None):
+    """Router logits [T, E] (f32 or bf16; -inf: expert not available) -> dict, with kk = k + shared and G = E + shared:
+    'experts' i32 and 'weights' f32 [T, kk], 'counts' i32 [G + 1] (rows of each group, then the routed tokens),
+    'group_offsets' i64 [G + 1], 'src' i32 [T kk], 'pos' i32 [T, kk], 'row_weights' f32 [T kk]; with aux also
+    'prob_sum' f32 [E] and 'loss' f32 [1].
+
+    group_offsets and src are the grouped GEMMs' and quantizers' row map (M = T kk).  token_mask (u8 or bool [T])
+    leaves padding tokens out: their experts, src and pos are -1.  See bsp_moe_route in include/bsp.h.
+    """
+    dt = _matrix_arg(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    kk, G = k + shared, E + shared
+    if k < 1 or shared < 0:
+        raise ValueError(f"k = {k} must be at least 1 and shared = {shared} at least 0")
+    if token_mask is not None:
+        _arg(token_mask, "token_mask", dev, ("u8", "bool"), T)
+    R = T * kk
+    if out is None:
+        i32, f32 = torch.int32, torch.float32
+        out = {"experts": torch.empty((T, kk), dtype=i32, device=dev),
+               "weights": torch.empty((T, kk), dtype=f32, device=dev),
+               "counts": torch.empty((G + 1,), dtype=i32, device=dev),
+               "group_offsets": torch.empty((G + 1,), dtype=torch.int64, device=dev),
+               "src": torch.empty((R,), dtype=i32, device=dev), "pos": torch.empty((T, kk), dtype=i32, device=dev),
+               "row_weights": torch.empty((R,), dtype=f32, device=dev)}
+        if aux:
+            out["prob_sum"] = torch.empty((E,), dtype=f32, device=dev)
+            out["loss"] = torch.empty((1,), dtype=f32, device=dev)
+    else:
+        for name, kind, need in (("experts", "i32", R), ("weights", "f32", R), ("counts", "i32", G + 1),
+                                 ("group_offsets", "i64", G + 1), ("src", "i32", R), ("pos", "i32", R),
+                                 ("row_weights", "f32", R)) + ((("prob_sum", "f32", E), ("loss", "f32", 1)) if aux
+                                                               else ()):
+            _arg(out.get(name), name, dev, kind, need)
+    need = moe_route_workspace_size(T, E, shared)
+    if workspace is not None:
+        _arg(workspace, "workspace", dev, "u8", need)
+    elif need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    st = _lib_raw().bsp_moe_route(
+        _ptr(logits), dt, T, E, _ld(logits), _ptr(token_mask), k, shared, _ptr(out["experts"]), _ptr(out["weights"]),
+        _ptr(out["counts"]), _ptr(out["group_offsets"]), _ptr(out["src"]), _ptr(out["pos"]), _ptr(out["row_weights"]),
+        _ptr(out["prob_sum"]) if aux else None, _ptr(out["loss"]) if aux else None, ROUTE_NORM if norm else 0,
+        _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(dev))
+    _check(st, "bsp_moe_route")
+    return out
+
+
+def moe_route_backward(logits: torch.Tensor, k: int, experts, counts, pos, d_weights=None, d_loss=None,
+                       norm: bool = True, shared: int = 0, token_mask=None, out=None):
+    """Gradient [T, E] (logits' dtype) of d_loss * loss + sum(d_weights * row_weights) to the logits, from the
+    forward call's experts, counts and pos.  d_weights f32 [T kk] is in grouped-row order, as
+    swiglu_checkpoint_backward returns it; d_loss is a device f32 scalar [1].  See bsp_moe_route_backward."""
+    dt = _matrix_arg(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    kk = k + shared
+    if k < 1 or shared < 0:
+        raise ValueError(f"k = {k} must be at least 1 and shared = {shared} at least 0")
+    if token_mask is not None:
+        _arg(token_mask, "token_mask", dev, ("u8", "bool"), T)
+    _arg(experts, "experts", dev, "i32", T * kk)
+    _arg(counts, "counts", dev, "i32", E + shared + 1)
+    _arg(pos, "pos", dev, "i32", T * kk)
+    _arg(d_weights, "d_weights", dev, "f32", T * kk, optional=True)
+    _arg(d_loss, "d_loss", dev, "f32", 1, optional=True)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    else:
+        _matrix_arg(out, "out", dev, logits.dtype)
+        if out.shape != logits.shape:
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(logits.shape)}")
+    st = _lib_raw().bsp_moe_route_backward(_ptr(logits), dt, T, E, _ld(logits), _ptr(token_mask), k, shared,
+                                           _ptr(experts), _ptr(pos), _ptr(counts), _ptr(d_weights), _ptr(d_loss),
+                                           _ptr(out), _ld(out), ROUTE_NORM if norm else 0, _stream(dev))
+    _check(st, "bsp_moe_route_backward")
+    return out
+
+
+def swiglu_checkpoint(h13: torch.Tensor, row_weights=None, n_rows=None, return_h: bool = True,
+                      quantize_h: bool = False, out=None):
+    """h13 [R, 2I] (f32 or bf16) -> dict: 'ckpt_codes' u8 [R, 2I] and 'ckpt_scales' u8 [R, 2I/32] (h13 as rowwise
+    MXFP8), 'h' bf16 [R, I] = row_weights * silu(gate) * up, and with quantize_h its rowwise MXFP8 'codes' [R, I]
+    and 'scales' [R, I/32].
+
+    n_rows: device i64 scalar, the rows in use (e.g. group_offsets[G:]); outputs of the others are zeros.
+    See bsp_swiglu_checkpoint in include/bsp.h.
+    """
+    _arg(h13, "h13", h13.device if isinstance(h13, torch.Tensor) else None, ("f32", "bf16"))
+    if h13.dim() != 2:
+        raise ValueError("h13 must be 2-D [R, 2I]")
+    R, I2 = h13.shape
+    if I2 % 64:
+        raise ValueError(f"h13 has {I2} columns, needs a multiple of 64")
+    I = I2 // 2
+    dev = h13.device
+    _arg(row_weights, "row_weights", dev, "f32", R, optional=True)
+    _arg(n_rows, "n_rows", dev, "i64", 1, optional=True)
+    if out is None:
+        out = {"ckpt_codes": torch.empty((R, I2), dtype=torch.uint8, device=dev),
+               "ckpt_scales": torch.empty((R, I2 // 32), dtype=torch.uint8, device=dev)}
+        if return_h:
+            out["h"] = torch.empty((R, I), dtype=torch.bfloat16, device=dev)
+        if quantize_h:
+            out["codes"] = torch.empty((R, I), dtype=torch.uint8, device=dev)
+            out["scales"] = torch.empty((R, I // 32), dtype=torch.uint8, device=dev)
+    else:
+        _arg(out.get("ckpt_codes"), "ckpt_codes", dev, "u8", R * I2)
+        _arg(out.get("ckpt_scales"), "ckpt_scales", dev, "u8", R * (I2 // 32))
+        _arg(out.get("h"), "h", dev, "bf16", R * I, optional=not return_h)
+        _arg(out.get("codes"), "codes", dev, "u8", R * I, optional=not quantize_h)
+        _arg(out.get("scales"), "scales", dev, "u8", R * (I // 32), optional=not quantize_h)
+    dt = DTYPE_BF16 if h13.dtype == torch.bfloat16 else DTYPE_F32
+    st = _lib_raw().bsp_swiglu_checkpoint(_ptr(h13), dt, R, I, _ptr(row_weights), _ptr(n_rows),
+                                          _ptr(out["h"]) if return_h else None,
+                                          _ptr(out["codes"]) if quantize_h else None,
+                                          _ptr(out["scales"]) if quantize_h else None, _ptr(out["ckpt_codes"]),
+                                          _ptr(out["ckpt_scales"]), _stream(dev))
+    _check(st, "bsp_swiglu_checkpoint")
+    return out
+
+
+def swiglu_checkpoint_backward(dh: torch.Tensor, ckpt_codes, ckpt_scales, row_weights=None, n_rows=None,
+                               return_h: bool = True, out=None):
+    """dh [R, I] (f32 or bf16) and the checkpoint -> dict: 'dh13' [R, 2I] in dh's dtype, 'h' bf16 [R, I] computed
+    again (unless return_h is False) and, with row_weights, 'd_row_weights' f32 [R].
+    See bsp_swiglu_checkpoint_backward in include/bsp.h."""
+    _arg(dh, "dh", dh.device if isinstance(dh, torch.Tensor) else None, ("f32", "bf16"))
+    if dh.dim() != 2 or dh.shape[1] % 32:
+        raise ValueError("dh must be 2-D [R, I] with I a multiple of 32")
+    R, I = dh.shape
+    dev = dh.device
+    _arg(ckpt_codes, "ckpt_codes", dev, "u8", R * 2 * I)
+    _arg(ckpt_scales, "ckpt_scales", dev, "u8", R * (2 * I // 32))
+    _arg(row_weights, "row_weights", dev, "f32", R, optional=True)
+    _arg(n_rows, "n_rows", dev, "i64", 1, optional=True)
+    weighted = row_weights is not None
+    if out is None:
+        out = {"dh13": torch.empty((R, 2 * I), dtype=dh.dtype, device=dev)}
+        if return_h:
+            out["h"] = torch.empty((R, I), dtype=torch.bfloat16, device=dev)
+        if weighted:
+            out["d_row_weights"] = torch.empty((R,), dtype=torch.float32, device=dev)
+    else:
+        _arg(out.get("dh13"), "dh13", dev, "bf16" if dh.dtype == torch.bfloat16 else "f32", R * 2 * I)
+        _arg(out.get("h"), "h", dev, "bf16", R * I, optional=not return_h)
+        _arg(out.get("d_row_weights"), "d_row_weights", dev, "f32", R, optional=not weighted)
+    dt = DTYPE_BF16 if dh.dtype == torch.bfloat16 else DTYPE_F32
+    st = _lib_raw().bsp_swiglu_checkpoint_backward(_ptr(dh), dt, R, I, _ptr(ckpt_codes), _ptr(ckpt_scales),
+                                                   _ptr(row_weights), _ptr(n_rows), _ptr(out["dh13"]),
+                                                   _ptr(out["h"]) if return_h else None,
+                                                   _ptr(out["d_row_weights"]) if weighted else None, _stream(dev))
+    _check(st, "bsp_swiglu_checkpoint_backward")
+    return out
+
+
+def moe_combine(y: torch.Tensor, pos, weights=None, out_dtype=None, out=None):
+    """y [rows, H] (f32 or bf16) -> [T, H]: the sum of rows pos[t, :] (negative or past the rows: nothing), each
+    times weights[t, :] if given.  pos i32 and weights f32 [T, kk], as moe_route returns them.
+    See bsp_moe_combine in include/bsp.h."""
+    di = _matrix_arg(y, "y")
+    rows, H = y.shape
+    dev = y.device
+    _arg(pos, "pos", dev, "i32")
+    if pos.dim() != 2:
+        raise ValueError("pos must be 2-D [T, kk]")
+    T, kk = pos.shape
+    _arg(weights, "weights", dev, "f32", T * kk, optional=True)
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype or y.dtype, device=dev)
+    do = _matrix_arg(out, "out", dev)
+    if out.shape != (T, H):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, H)}")
+    st = _lib_raw().bsp_moe_combine(_ptr(y), di, rows, H, _ld(y), _ptr(pos), _ptr(weights), T, kk, _ptr(out), do,
+                                    _ld(out), _stream(dev))
+    _check(st, "bsp_moe_combine")
+    return out

@@ -18,7 +18,10 @@
  *     weight gradient) [alphasignal.ai, Recipe 1 and Recipe 2];
  *   - the BF16 grouped expert GEMM of the NVFP4 recipe's backward pass, on the
  *     original or on dequantized operands [remio.ai, section "Entrambe le
- *     ricette supportano ..."; alphasignal.ai, Recipe 2].
+ *     ricette supportano ..."; alphasignal.ai, Recipe 2];
+ *   - what joins these into a layer: routing with the load-balance loss and
+ *     its gradients, SwiGLU with an 8-bit checkpoint of its input and its
+ *     backward pass, and the sum of a token's expert outputs.
  *
  * Conventions shared by every call:
  *   - Pointers named in the comments as "device" point to GPU memory; sizes
@@ -72,6 +75,7 @@ enum { BSP_GEMM_FPROP = 0, BSP_GEMM_DGRAD = 1, BSP_GEMM_WGRAD = 2 };
 /* flags */
 #define BSP_NVFP4_46 0x1u /* NVFP4: choose between the "6" and "4" block scales */
 #define BSP_SR 0x2u       /* requant: stochastic rounding (else nearest even) */
+#define BSP_ROUTE_NORM 0x4u /* routing: weights divided by their sum over the chosen experts */
 
 int bsp_version(void);                    /* 100 * major + minor */
 const char *bsp_status_string(int status); /* static string, never NULL */
@@ -431,6 +435,128 @@ bsp_status bsp_moe_grouped_gemm_bf16_tiled(int mode, const uint16_t *a, int64_t 
 bsp_status bsp_swiglu_quantize(const void *h13, int in_dtype, int64_t R, int64_t I, uint16_t *h_out, int fmt,
                                uint8_t *codes, uint8_t *scales, float *outer, uint32_t flags, void *stream);
 
+/*
+ * MoE routing: from router logits to everything the grouped GEMMs and the
+ * training loss take [hackernews.jp, "4ビットの教訓", footnote 5: top-8 of 128
+ * experts; alphasignal.ai, Results: Qwen3-30B-A3B].  The expert choice, the
+ * weights, the per-expert counts, the grouped-row map and the load-balance
+ * loss come from one call and no host synchronization.
+ *
+ *   logits   device [T, ldl >= E] of dtype (BSP_DTYPE_F32 or BSP_DTYPE_BF16);
+ *            -inf marks an expert the token may not take
+ *   T, E     1 <= E <= 1024; k experts per token, 1 <= k <= min(E, 32);
+ *            `shared` (0..64) further groups that every routed token joins with
+ *            weight 1.  kk = k + shared, G = E + shared, T * kk < 2^31.
+ *   token_mask  device u8 [T] or NULL: 0 = padding token; its logits are not
+ *            read and it takes no row.  A token is routed when its mask is not
+ *            0 and some logit is above -inf.
+ *   flags    0 or BSP_ROUTE_NORM
+ *   experts  device int32 [T, kk] (out): the k largest logits in decreasing
+ *            order, equal ones by index (-0 equals +0), then E, .., G - 1; -1
+ *            where the token is not routed or has no further expert
+ *   weights  device f32 [T, kk] (out): softmax(logits) of the choice; with
+ *            BSP_ROUTE_NORM divided by its sum over the k; 1 for shared
+ *            groups; 0 where experts is -1
+ *   counts   device int32 [G + 1] (out): rows of each group, then the number
+ *            n of routed tokens
+ *   group_offsets  device int64 [G + 1] (out): running sum of the counts
+ *   src      device int32 [T kk] (out): token of each grouped row; rows are
+ *            ordered by group, then by token; -1 from group_offsets[G] on
+ *   pos      device int32 [T, kk] (out): the grouped row of each choice, or -1
+ *   row_weights  device f32 [T kk] (out): weight of each grouped row, 0 from
+ *            group_offsets[G] on
+ *   prob_sum device f32 [E] or NULL (out): Q_e, the sum of the routed tokens'
+ *            softmax probabilities of expert e
+ *   loss     device f32 [1] or NULL (out; both or neither):
+ *            E / (k n^2) sum_{e < E} counts_e Q_e (1 when both are uniform; 0
+ *            for n = 0)
+ *   workspace  device, >= bsp_moe_route_workspace_size(T, E, shared) bytes
+ * group_offsets and src are the grouped GEMMs' and quantizers' row map with
+ * M = T kk; with padding tokens group_offsets[G] < M, and those calls leave
+ * the rows of C past it untouched.  Sums are f32 in a fixed order: results
+ * are the same on every run.  A row with NaN or +inf logits is not routed; its
+ * k weights, prob_sum and loss become NaN.
+ *
+ * bsp_moe_route_backward: the gradient to the logits of
+ *   d_loss * loss + sum_{t, j < k} d_weights[pos[t, j]] * weights[t, j]
+ * with the counts held constant.
+ *   logits .. shared, flags  as in the forward call
+ *   experts, pos  device int32 [T, kk], as the forward call wrote them
+ *   counts   device int32 [G + 1].  Data-parallel training passes the sums of
+ *            all ranks' counts: the gradient is then that of the global loss.
+ *   d_weights  device f32 [T kk] in grouped-row order (as
+ *            bsp_swiglu_checkpoint_backward writes d_row_weights) or NULL;
+ *            entries of shared groups are ignored
+ *   d_loss   device f32 [1] or NULL (not both NULL)
+ *   d_logits device [T, ldd >= E] of dtype (out); rows of tokens that are not
+ *            routed are zeros
+ * The probabilities are recomputed from the logits.
+ */
+bsp_status bsp_moe_route(const void *logits, int dtype, int64_t T, int64_t E, int64_t ldl, const uint8_t *token_mask,
+                         int64_t k, int64_t shared, int32_t *experts, float *weights, int32_t *counts,
+                         int64_t *group_offsets, int32_t *src, int32_t *pos, float *row_weights, float *prob_sum,
+                         float *loss, uint32_t flags, void *workspace, size_t ws_bytes, void *stream);
+bsp_status bsp_moe_route_backward(const void *logits, int dtype, int64_t T, int64_t E, int64_t ldl,
+                                  const uint8_t *token_mask, int64_t k, int64_t shared, const int32_t *experts,
+                                  const int32_t *pos, const int32_t *counts, const float *d_weights,
+                                  const float *d_loss, void *d_logits, int64_t ldd, uint32_t flags, void *stream);
+
+/*
+ * SwiGLU with its input kept in 8 bits, and its backward pass from there.
+ * The gate/up product h13 is the largest activation a MoE layer keeps for the
+ * backward pass; as MXFP8 it takes 1.03 instead of 2 or 4 bytes per value, and
+ * h is computed again instead of kept [alphasignal.ai, Recipe 1: the same
+ * format as the layer's operands].
+ *
+ * bsp_swiglu_checkpoint:
+ *   h13      device [R, 2I] of in_dtype (f32 or bf16): gate = columns [0, I),
+ *            up = columns [I, 2I); I % 32 == 0
+ *   row_weights  device f32 [R] or NULL (1): the router's weight of each row,
+ *            applied to h rather than to the down projection's output, so that
+ *            the latter need not be kept for the weight's gradient
+ *   n_rows   device int64 [1] or NULL (R): rows in use, e.g. group_offsets + G;
+ *            rows from it on are not read and their outputs are zeros (8-byte
+ *            aligned)
+ *   h_out    device bf16 [R, I] or NULL (out): bf16(row_weights * silu(gate) * up)
+ *   codes, scales  device u8 [R, I], [R, I/32], or both NULL (out): h as
+ *            rowwise MXFP8.  h_out or codes must be given.
+ *   ckpt_codes, ckpt_scales  device u8 [R, 2I], [R, 2I/32] (out): h13 as
+ *            rowwise MXFP8, blocks and rounding as bsp_quantize_mxfp8
+ * h is computed from h13 itself; the checkpoint serves the backward pass.
+ *
+ * bsp_swiglu_checkpoint_backward:
+ *   dh       device [R, I] of dtype (f32 or bf16): gradient of h
+ *   ckpt_codes, ckpt_scales, row_weights, n_rows  as above
+ *   dh13     device [R, 2I] of dtype (out): gradient of gate and up
+ *   h_out    device bf16 [R, I] or NULL (out): h computed again, for the down
+ *            projection's weight gradient
+ *   d_row_weights  device f32 [R] or NULL (out): sum_i dh_i silu(gate_i) up_i
+ * with gate and up the checkpoint's values, s = 1 / (1 + exp(-gate)) and
+ * w the row's weight: d up = w dh gate s, d gate = w dh up s (1 + gate (1 - s)).
+ */
+bsp_status bsp_swiglu_checkpoint(const void *h13, int in_dtype, int64_t R, int64_t I, const float *row_weights,
+                                 const int64_t *n_rows, uint16_t *h_out, uint8_t *codes, uint8_t *scales,
+                                 uint8_t *ckpt_codes, uint8_t *ckpt_scales, void *stream);
+bsp_status bsp_swiglu_checkpoint_backward(const void *dh, int dtype, int64_t R, int64_t I, const uint8_t *ckpt_codes,
+                                          const uint8_t *ckpt_scales, const float *row_weights,
+                                          const int64_t *n_rows, void *dh13, uint16_t *h_out, float *d_row_weights,
+                                          void *stream);
+
+/*
+ * Sum of every token's grouped rows: the layer's output from the down
+ * projection, and the input's gradient from the gate/up data gradient.
+ *   out[t, :] = sum_j weights[t, j] * y[pos[t, j], :]   (f32, in order of j)
+ *   y        device [rows, ldy >= H] of in_dtype (f32 or bf16)
+ *   pos      device int32 [T, kk], 1 <= kk <= 128; an index outside [0, rows)
+ *            contributes nothing (and nothing is read for it)
+ *   weights  device f32 [T, kk] or NULL (all 1)
+ *   out      device [T, ldo >= H] of out_dtype (f32 or bf16)
+ *   H, ldy, ldo multiples of 8
+ */
+bsp_status bsp_moe_combine(const void *y, int in_dtype, int64_t rows, int64_t H, int64_t ldy, const int32_t *pos,
+                           const float *weights, int64_t T, int64_t kk, void *out, int out_dtype, int64_t ldo,
+                           void *stream);
+
 /* Host-only size helpers (pure functions, no HIP calls). */
 bsp_status bsp_nvfp4_sizes(int64_t M, int64_t K, int64_t rows_per_scale, size_t *codes_bytes,
                            size_t *scales_bytes, size_t *outer_count);
@@ -454,6 +580,9 @@ size_t bsp_requant_batched_workspace_size(int64_t E, int64_t M, int64_t rows_per
 size_t bsp_gemm_workspace_size(int fmt, int mode, int64_t M, int64_t N, int64_t K, int64_t G);
 /* Bytes of workspace for bsp_moe_grouped_gemm_bf16 (0 for invalid arguments). */
 size_t bsp_gemm_bf16_workspace_size(int mode, int64_t M, int64_t N, int64_t K, int64_t G);
+/* Bytes of workspace for bsp_moe_route (0 for invalid arguments, and for
+ * batches small enough to need none). */
+size_t bsp_moe_route_workspace_size(int64_t T, int64_t E, int64_t shared);
 
 #ifdef __cplusplus
 }
