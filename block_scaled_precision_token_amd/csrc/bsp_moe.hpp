@@ -37,6 +37,13 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
+// Two bf16 (a in the low half), nearest even, by V_CVT_PK_BF16_F32.
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, b2));
+}
+
 // Eight consecutive values (16-byte aligned) as f32, and back (bf16: nearest even).
 __device__ __forceinline__ void ld8(const float *p, float (&v)[8]) {
     const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
@@ -57,10 +64,8 @@ __device__ __forceinline__ void st8(float *p, const float (&v)[8]) {
     *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 __device__ __forceinline__ void st8(uint16_t *p, const float (&v)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) w[i] = f32_to_bf16(v[2 * i]) | (f32_to_bf16(v[2 * i + 1]) << 16);
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                                               bf16x2(v[6], v[7]));
 }
 
 }  // namespace bsp

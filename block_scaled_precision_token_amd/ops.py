@@ -136,8 +136,14 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """The current stream's handle, without building a Stream object for it where torch allows (2 us a call)."""
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 # Device type the tensor arguments must live on.  The CPU tests of the
@@ -636,20 +642,41 @@ def swiglu_quantize(h13: torch.Tensor, fmt: int = -1, mode46: bool = False, retu
 # routing, SwiGLU checkpoint, combine
 # ---------------------------------------------------------------------------
 
+def _dev_ptr(t, name, dev, kind, numel):
+    """_arg for a required contiguous tensor of one dtype, in one expression when all is well (a call for a single
+    token is bound by such checks); returns the pointer."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _DT[kind] and t.device == dev and t.is_contiguous()
+            and t.numel() >= numel):
+        _arg(t, name, dev, kind, numel)
+    return t.data_ptr()
+
+
+def _opt_ptr(t, name, dev, kind, numel):
+    return None if t is None else _dev_ptr(t, name, dev, kind, numel)
+
+
+def _mask_ptr(token_mask, dev, T):
+    if token_mask is None:
+        return None
+    _arg(token_mask, "token_mask", dev, ("u8", "bool"), T)
+    return token_mask.data_ptr()
+
+
 def _matrix_arg(t, name, dev=None, dtype=None):
     """A 2-D f32 or bf16 tensor with unit column stride; returns its C dtype."""
     _need_cuda(t, name)
     _rowmajor(t, name)
-    if t.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and t.dtype != dtype):
+    if t.dtype is not torch.float32 and t.dtype is not torch.bfloat16 or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{name} must have dtype {dtype or 'f32 or bf16'}, not {t.dtype}")
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    return DTYPE_BF16 if t.dtype == torch.bfloat16 else DTYPE_F32
+    return DTYPE_BF16 if t.dtype is torch.bfloat16 else DTYPE_F32
 
 
 def _ld(t):
     """Row stride of a 2-D tensor; torch leaves a single row's stride free."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    ld, cols = t.stride(0), t.shape[1]
+    return ld if ld >= cols or t.shape[0] > 1 else cols
 
 
 def moe_route_workspace_size(T: int, E: int, shared: int = 0) -> int:
@@ -672,8 +699,7 @@ def moe_route(logits: torch.Tensor, k: int, norm: bool = True, shared: int = 0, 
     kk, G = k + shared, E + shared
     if k < 1 or shared < 0:
         raise ValueError(f"k = {k} must be at least 1 and shared = {shared} at least 0")
-    if token_mask is not None:
-        _arg(token_mask, "token_mask", dev, ("u8", "bool"), T)
+    mask = _mask_ptr(token_mask, dev, T)
     R = T * kk
     if out is None:
         i32, f32 = torch.int32, torch.float32
@@ -686,22 +712,21 @@ def moe_route(logits: torch.Tensor, k: int, norm: bool = True, shared: int = 0, 
         if aux:
             out["prob_sum"] = torch.empty((E,), dtype=f32, device=dev)
             out["loss"] = torch.empty((1,), dtype=f32, device=dev)
-    else:
-        for name, kind, need in (("experts", "i32", R), ("weights", "f32", R), ("counts", "i32", G + 1),
-                                 ("group_offsets", "i64", G + 1), ("src", "i32", R), ("pos", "i32", R),
-                                 ("row_weights", "f32", R)) + ((("prob_sum", "f32", E), ("loss", "f32", 1)) if aux
-                                                               else ()):
-            _arg(out.get(name), name, dev, kind, need)
-    need = moe_route_workspace_size(T, E, shared)
-    if workspace is not None:
-        _arg(workspace, "workspace", dev, "u8", need)
-    elif need:
+    get = out.get
+    ptrs = (_dev_ptr(get("experts"), "experts", dev, "i32", R), _dev_ptr(get("weights"), "weights", dev, "f32", R),
+            _dev_ptr(get("counts"), "counts", dev, "i32", G + 1),
+            _dev_ptr(get("group_offsets"), "group_offsets", dev, "i64", G + 1),
+            _dev_ptr(get("src"), "src", dev, "i32", R), _dev_ptr(get("pos"), "pos", dev, "i32", R),
+            _dev_ptr(get("row_weights"), "row_weights", dev, "f32", R),
+            _dev_ptr(get("prob_sum"), "prob_sum", dev, "f32", E) if aux else None,
+            _dev_ptr(get("loss"), "loss", dev, "f32", 1) if aux else None)
+    lib = _lib_raw()
+    need = lib.bsp_moe_route_workspace_size(T, E, shared)
+    if workspace is None and need:
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    st = _lib_raw().bsp_moe_route(
-        _ptr(logits), dt, T, E, _ld(logits), _ptr(token_mask), k, shared, _ptr(out["experts"]), _ptr(out["weights"]),
-        _ptr(out["counts"]), _ptr(out["group_offsets"]), _ptr(out["src"]), _ptr(out["pos"]), _ptr(out["row_weights"]),
-        _ptr(out["prob_sum"]) if aux else None, _ptr(out["loss"]) if aux else None, ROUTE_NORM if norm else 0,
-        _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(dev))
+    ws = _opt_ptr(workspace, "workspace", dev, "u8", need)
+    st = lib.bsp_moe_route(logits.data_ptr(), dt, T, E, _ld(logits), mask, k, shared, *ptrs, ROUTE_NORM if norm else 0,
+                           ws, need, _stream(dev))
     _check(st, "bsp_moe_route")
     return out
 
@@ -717,22 +742,18 @@ def moe_route_backward(logits: torch.Tensor, k: int, experts, counts, pos, d_wei
     kk = k + shared
     if k < 1 or shared < 0:
         raise ValueError(f"k = {k} must be at least 1 and shared = {shared} at least 0")
-    if token_mask is not None:
-        _arg(token_mask, "token_mask", dev, ("u8", "bool"), T)
-    _arg(experts, "experts", dev, "i32", T * kk)
-    _arg(counts, "counts", dev, "i32", E + shared + 1)
-    _arg(pos, "pos", dev, "i32", T * kk)
-    _arg(d_weights, "d_weights", dev, "f32", T * kk, optional=True)
-    _arg(d_loss, "d_loss", dev, "f32", 1, optional=True)
+    mask = _mask_ptr(token_mask, dev, T)
+    ptrs = (_dev_ptr(experts, "experts", dev, "i32", T * kk), _dev_ptr(pos, "pos", dev, "i32", T * kk),
+            _dev_ptr(counts, "counts", dev, "i32", E + shared + 1),
+            _opt_ptr(d_weights, "d_weights", dev, "f32", T * kk), _opt_ptr(d_loss, "d_loss", dev, "f32", 1))
     if out is None:
         out = torch.empty((T, E), dtype=logits.dtype, device=dev)
     else:
         _matrix_arg(out, "out", dev, logits.dtype)
         if out.shape != logits.shape:
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(logits.shape)}")
-    st = _lib_raw().bsp_moe_route_backward(_ptr(logits), dt, T, E, _ld(logits), _ptr(token_mask), k, shared,
-                                           _ptr(experts), _ptr(pos), _ptr(counts), _ptr(d_weights), _ptr(d_loss),
-                                           _ptr(out), _ld(out), ROUTE_NORM if norm else 0, _stream(dev))
+    st = _lib_raw().bsp_moe_route_backward(logits.data_ptr(), dt, T, E, _ld(logits), mask, k, shared, *ptrs,
+                                           out.data_ptr(), _ld(out), ROUTE_NORM if norm else 0, _stream(dev))
     _check(st, "bsp_moe_route_backward")
     return out
 
@@ -754,8 +775,8 @@ def swiglu_checkpoint(h13: torch.Tensor, row_weights=None, n_rows=None, return_h
         raise ValueError(f"h13 has {I2} columns, needs a multiple of 64")
     I = I2 // 2
     dev = h13.device
-    _arg(row_weights, "row_weights", dev, "f32", R, optional=True)
-    _arg(n_rows, "n_rows", dev, "i64", 1, optional=True)
+    rw = _opt_ptr(row_weights, "row_weights", dev, "f32", R)
+    nr = _opt_ptr(n_rows, "n_rows", dev, "i64", 1)
     if out is None:
         out = {"ckpt_codes": torch.empty((R, I2), dtype=torch.uint8, device=dev),
                "ckpt_scales": torch.empty((R, I2 // 32), dtype=torch.uint8, device=dev)}
@@ -764,18 +785,14 @@ def swiglu_checkpoint(h13: torch.Tensor, row_weights=None, n_rows=None, return_h
         if quantize_h:
             out["codes"] = torch.empty((R, I), dtype=torch.uint8, device=dev)
             out["scales"] = torch.empty((R, I // 32), dtype=torch.uint8, device=dev)
-    else:
-        _arg(out.get("ckpt_codes"), "ckpt_codes", dev, "u8", R * I2)
-        _arg(out.get("ckpt_scales"), "ckpt_scales", dev, "u8", R * (I2 // 32))
-        _arg(out.get("h"), "h", dev, "bf16", R * I, optional=not return_h)
-        _arg(out.get("codes"), "codes", dev, "u8", R * I, optional=not quantize_h)
-        _arg(out.get("scales"), "scales", dev, "u8", R * (I // 32), optional=not quantize_h)
+    get = out.get
+    ptrs = (_dev_ptr(get("h"), "h", dev, "bf16", R * I) if return_h else None,
+            _dev_ptr(get("codes"), "codes", dev, "u8", R * I) if quantize_h else None,
+            _dev_ptr(get("scales"), "scales", dev, "u8", R * (I // 32)) if quantize_h else None,
+            _dev_ptr(get("ckpt_codes"), "ckpt_codes", dev, "u8", R * I2),
+            _dev_ptr(get("ckpt_scales"), "ckpt_scales", dev, "u8", R * (I2 // 32)))
     dt = DTYPE_BF16 if h13.dtype == torch.bfloat16 else DTYPE_F32
-    st = _lib_raw().bsp_swiglu_checkpoint(_ptr(h13), dt, R, I, _ptr(row_weights), _ptr(n_rows),
-                                          _ptr(out["h"]) if return_h else None,
-                                          _ptr(out["codes"]) if quantize_h else None,
-                                          _ptr(out["scales"]) if quantize_h else None, _ptr(out["ckpt_codes"]),
-                                          _ptr(out["ckpt_scales"]), _stream(dev))
+    st = _lib_raw().bsp_swiglu_checkpoint(h13.data_ptr(), dt, R, I, rw, nr, *ptrs, _stream(dev))
     _check(st, "bsp_swiglu_checkpoint")
     return out
 
@@ -790,10 +807,10 @@ def swiglu_checkpoint_backward(dh: torch.Tensor, ckpt_codes, ckpt_scales, row_we
         raise ValueError("dh must be 2-D [R, I] with I a multiple of 32")
     R, I = dh.shape
     dev = dh.device
-    _arg(ckpt_codes, "ckpt_codes", dev, "u8", R * 2 * I)
-    _arg(ckpt_scales, "ckpt_scales", dev, "u8", R * (2 * I // 32))
-    _arg(row_weights, "row_weights", dev, "f32", R, optional=True)
-    _arg(n_rows, "n_rows", dev, "i64", 1, optional=True)
+    cc = _dev_ptr(ckpt_codes, "ckpt_codes", dev, "u8", R * 2 * I)
+    cs = _dev_ptr(ckpt_scales, "ckpt_scales", dev, "u8", R * (2 * I // 32))
+    rw = _opt_ptr(row_weights, "row_weights", dev, "f32", R)
+    nr = _opt_ptr(n_rows, "n_rows", dev, "i64", 1)
     weighted = row_weights is not None
     if out is None:
         out = {"dh13": torch.empty((R, 2 * I), dtype=dh.dtype, device=dev)}
@@ -801,15 +818,13 @@ def swiglu_checkpoint_backward(dh: torch.Tensor, ckpt_codes, ckpt_scales, row_we
             out["h"] = torch.empty((R, I), dtype=torch.bfloat16, device=dev)
         if weighted:
             out["d_row_weights"] = torch.empty((R,), dtype=torch.float32, device=dev)
-    else:
-        _arg(out.get("dh13"), "dh13", dev, "bf16" if dh.dtype == torch.bfloat16 else "f32", R * 2 * I)
-        _arg(out.get("h"), "h", dev, "bf16", R * I, optional=not return_h)
-        _arg(out.get("d_row_weights"), "d_row_weights", dev, "f32", R, optional=not weighted)
-    dt = DTYPE_BF16 if dh.dtype == torch.bfloat16 else DTYPE_F32
-    st = _lib_raw().bsp_swiglu_checkpoint_backward(_ptr(dh), dt, R, I, _ptr(ckpt_codes), _ptr(ckpt_scales),
-                                                   _ptr(row_weights), _ptr(n_rows), _ptr(out["dh13"]),
-                                                   _ptr(out["h"]) if return_h else None,
-                                                   _ptr(out["d_row_weights"]) if weighted else None, _stream(dev))
+    bf = dh.dtype == torch.bfloat16
+    get = out.get
+    ptrs = (_dev_ptr(get("dh13"), "dh13", dev, "bf16" if bf else "f32", R * 2 * I),
+            _dev_ptr(get("h"), "h", dev, "bf16", R * I) if return_h else None,
+            _dev_ptr(get("d_row_weights"), "d_row_weights", dev, "f32", R) if weighted else None)
+    st = _lib_raw().bsp_swiglu_checkpoint_backward(dh.data_ptr(), DTYPE_BF16 if bf else DTYPE_F32, R, I, cc, cs, rw,
+                                                   nr, *ptrs, _stream(dev))
     _check(st, "bsp_swiglu_checkpoint_backward")
     return out
 
@@ -821,17 +836,17 @@ def moe_combine(y: torch.Tensor, pos, weights=None, out_dtype=None, out=None):
     di = _matrix_arg(y, "y")
     rows, H = y.shape
     dev = y.device
-    _arg(pos, "pos", dev, "i32")
-    if pos.dim() != 2:
+    if not isinstance(pos, torch.Tensor) or pos.dim() != 2:
         raise ValueError("pos must be 2-D [T, kk]")
     T, kk = pos.shape
-    _arg(weights, "weights", dev, "f32", T * kk, optional=True)
+    pp = _dev_ptr(pos, "pos", dev, "i32", T * kk)
+    wp = _opt_ptr(weights, "weights", dev, "f32", T * kk)
     if out is None:
         out = torch.empty((T, H), dtype=out_dtype or y.dtype, device=dev)
     do = _matrix_arg(out, "out", dev)
     if out.shape != (T, H):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, H)}")
-    st = _lib_raw().bsp_moe_combine(_ptr(y), di, rows, H, _ld(y), _ptr(pos), _ptr(weights), T, kk, _ptr(out), do,
-                                    _ld(out), _stream(dev))
+    st = _lib_raw().bsp_moe_combine(y.data_ptr(), di, rows, H, _ld(y), pp, wp, T, kk, out.data_ptr(), do, _ld(out),
+                                    _stream(dev))
     _check(st, "bsp_moe_combine")
     return out
