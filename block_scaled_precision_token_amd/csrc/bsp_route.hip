@@ -15,12 +15,11 @@ namespace bsp {
 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr int64_t kManyTokens = 32768;
-constexpr int64_t kBwdWorkgroups = 1280;
-constexpr int kRouteThreads = 512;   // workgroup of the placing
-constexpr int kWords = 8;            // placing: tokens ranked at a time, in words of 32
+constexpr int64_t kBwdWorkgroups = 1024;
 constexpr int64_t kOneWorkgroupTokens = 64;
 constexpr int kMaxShared = 64;
 constexpr int kMaxGroups = 1024 + kMaxShared;
+constexpr int kManyWordsGroups = kMaxGroups / 2;   // groups of the widest rank table
 
 // Lane exchanges within a row of 16 by DPP.  A token's L lanes (4, 8, 16 or 32)
 // reduce over mirror(16), mirror(8), xor 2, xor 1, each step joining two
@@ -64,19 +63,6 @@ __device__ __forceinline__ float elem(const float *p) { return *p; }
 __device__ __forceinline__ float elem(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t *p, float v) { *p = (uint16_t)bf16x2(v, 0.0f); }
-__device__ __forceinline__ void ld16(const float *p, float *v) {
-    const float4 f = *reinterpret_cast<const float4 *>(p);
-    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-}
-__device__ __forceinline__ void ld16(const uint16_t *p, float *v) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        v[2 * i] = bf16_lo(w[i]);
-        v[2 * i + 1] = bf16_hi(w[i]);
-    }
-}
 __device__ __forceinline__ void st16(float *p, const float *v) {
     *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
@@ -84,22 +70,55 @@ __device__ __forceinline__ void st16(uint16_t *p, const float *v) {
     *reinterpret_cast<uint4 *>(p) = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
                                                bf16x2(v[6], v[7]));
 }
-// -inf past E.  VEC: rows start on 16 bytes and E is a multiple of Q, so a
-// piece is whole or absent.
+// A row's V logits as loaded.  Every load is issued, those past E from the
+// row's start, and what is not wanted becomes -inf afterwards: a load under a
+// condition would be waited for before the next.  VEC: rows start on 16 bytes
+// and E is a multiple of Q, so a piece is whole or absent.
 template <typename T, int L, int V, bool VEC>
-__device__ __forceinline__ void load_logits(const T *row, int lane, int E, float (&v)[V]) {
-    constexpr int Q = kPiece<T>;
+struct RowLoad {
+    static constexpr int Q = kPiece<T>;
+    uint4 r[VEC ? V / Q : 1];
+    T x[VEC ? 1 : V];
+    __device__ __forceinline__ void load(const T *row, int lane, int E) {
+        if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < V; i += Q) {
-        const int e = expert_of<T, L>(lane, i);
-        if (VEC && e < E) {
-            ld16(row + e, v + i);
+            for (int j = 0; j < V / Q; j++) {
+                const int e = expert_of<T, L>(lane, j * Q);
+                r[j] = *reinterpret_cast<const uint4 *>(row + (e < E ? e : 0));
+            }
         } else {
 #pragma unroll
-            for (int q = 0; q < Q; q++) v[i + q] = !VEC && e + q < E ? elem(row + e + q) : -INFINITY;
+            for (int i = 0; i < V; i++) {
+                const int e = expert_of<T, L>(lane, i);
+                x[i] = row[e < E ? e : 0];
+            }
         }
     }
-}
+    __device__ __forceinline__ void get(int lane, int E, bool keep, float (&v)[V]) const {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int j = 0; j < V / Q; j++) {
+                const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    if constexpr (Q == 4) {
+                        v[j * Q + i] = __uint_as_float(w[i]);
+                    } else {
+                        v[j * Q + 2 * i] = bf16_lo(w[i]);
+                        v[j * Q + 2 * i + 1] = bf16_hi(w[i]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++) v[i] = elem(&x[i]);
+        }
+        if (E < L * V || !keep) {
+#pragma unroll
+            for (int i = 0; i < V; i++) v[i] = keep && expert_of<T, L>(lane, i) < E ? v[i] : -INFINITY;
+        }
+    }
+};
 template <typename T, int L, int V, bool VEC>
 __device__ __forceinline__ void store_logits(T *row, int lane, int E, const float (&v)[V]) {
     constexpr int Q = kPiece<T>;
@@ -251,7 +270,8 @@ struct RouteArgs {
     int64_t *off;
     // workspace, one entry per workgroup (a run of CT consecutive tokens)
     int32_t CT, nwg, ldh, lde;
-    int32_t *hist;    // [nwg][ldh]: rows of each group, routed tokens, zeros
+    void *hist;       // rows of each group, then routed tokens, zeros up to ldh; u8 or (CT > 255) u16,
+                      // in 16-byte pieces of columns: [piece][nwg][16 bytes]
     float *part;      // [nwg][lde]: sums of probabilities, zeros
 };
 
@@ -272,17 +292,15 @@ __device__ __forceinline__ void route_select(const RouteArgs &a, int64_t t0, int
 #pragma unroll
     for (int i = 0; i < V; i++) acc[i] = 0.0f;
     for (int64_t t = t0 + grp; t < t1; t += BT / L) {
+        RowLoad<T, L, V, VEC> in;
+        in.load(reinterpret_cast<const T *>(a.logits) + t * a.ldl, lane, a.E);
+        const bool keep = !a.mask || a.mask[t];
         float v[V];
-        if (!a.mask || a.mask[t]) {
-            load_logits<T, L, V, VEC>(reinterpret_cast<const T *>(a.logits) + t * a.ldl, lane, a.E, v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; i++) v[i] = -INFINITY;
-        }
+        in.get(lane, a.E, keep, v);
         double top[N];
         top_keys<T, L, V, N>(v, lane, top);
         const float best = key_logit(top[0]), m = best > -INFINITY ? best : 0.0f;
-        const float sum = exp_sum<L>(v, m), inv = 1.0f / sum;
+        const float sum = exp_sum<L>(v, m), inv = __builtin_amdgcn_rcpf(sum);   // sum >= 1 where routed
         const bool routed = sum > 0.0f, bad = sum != sum;
         if (aux && sum != 0.0f) {             // NaN in a bad row reaches prob_sum and loss
 #pragma unroll
@@ -303,7 +321,7 @@ __device__ __forceinline__ void route_select(const RouteArgs &a, int64_t t0, int
             total += val[q];
         }
         total = group_sum<L>(total);
-        const float scale = bad ? sum : !routed ? 0.0f : a.norm ? 1.0f / total : inv;
+        const float scale = bad ? sum : !routed ? 0.0f : a.norm ? __builtin_amdgcn_rcpf(total) : inv;
 #pragma unroll
         for (int q = 0; q < KS; q++) {
             const int j = q * L + lane;
@@ -348,11 +366,24 @@ __device__ __forceinline__ void route_select(const RouteArgs &a, int64_t t0, int
             }
         }
         __syncthreads();
-        for (int e = tid; e < a.E; e += BT) {
-            float s = 0.0f;
-#pragma unroll 8
-            for (int w = 0; w < kSumRows<L, BT>; w++) s += psum[w * a.E + e];
-            psum[e] = s;
+        // the rows in `parts` interleaved shares, then the shares
+        const int parts = BT / a.E < 1 ? 1 : BT / a.E < 8 ? BT / a.E : 8;
+        float s[BT < L * V ? L * V / BT : 1];
+#pragma unroll
+        for (int c = 0; c < (BT < L * V ? L * V / BT : 1); c++) {
+            const int i = c * BT + tid, q = i / a.E, e = i - q * a.E;
+            s[c] = 0.0f;
+            if (q < parts)
+                for (int w = q; w < kSumRows<L, BT>; w += parts) s[c] += psum[w * a.E + e];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < (BT < L * V ? L * V / BT : 1); c++)
+            if (c * BT + tid < parts * a.E) psum[c * BT + tid] = s[c];
+        __syncthreads();
+        if (parts > 1 && tid < a.E) {
+            for (int q = 1; q < parts; q++) s[0] += psum[q * a.E + tid];
+            psum[tid] = s[0];
         }
     }
     __syncthreads();
@@ -375,87 +406,182 @@ __device__ void route_loss(const RouteArgs &a, const int32_t *tot, const float *
     }
 }
 
-// Group starts: exclusive scan of tot[0, G) into base (LDS), by the first
-// wavefront; base[G] is the rows in use.
-__device__ void route_starts(const RouteArgs &a, const int32_t *tot, int32_t *base) {
+// Inclusive sum over the lanes up to this one, by DPP: within rows of 16, then
+// the rows' totals to the rows after them.
+__device__ __forceinline__ int32_t wave_scan(int32_t v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);    // row_shr 1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // lane 15 of a row to the next row
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // lane 31 to the upper rows
+    return v;
+}
+
+// Sum over a row of 16 lanes, on all of them.
+__device__ __forceinline__ uint32_t row_sum(uint32_t v) {
+    v += (uint32_t)__builtin_amdgcn_mov_dpp((int)v, DPP_MIRROR16, 0xF, 0xF, true);
+    v += (uint32_t)__builtin_amdgcn_mov_dpp((int)v, DPP_MIRROR8, 0xF, 0xF, true);
+    v += (uint32_t)__builtin_amdgcn_mov_dpp((int)v, DPP_XOR2, 0xF, 0xF, true);
+    v += (uint32_t)__builtin_amdgcn_mov_dpp((int)v, DPP_XOR1, 0xF, 0xF, true);
+    return v;
+}
+
+// Exclusive scan of in[0, n) into out[0, n] (LDS, may be the same), the total
+// last, by the first wavefront; the caller synchronizes.
+__device__ __forceinline__ void exclusive_scan(const int32_t *in, int32_t *out, int n) {
     if (threadIdx.x >= 64) return;
-    const int lane = threadIdx.x;
-    int32_t carry = 0;
-    for (int g0 = 0; g0 <= a.G; g0 += 64) {
-        const int g = g0 + lane;
-        const int32_t c = g < a.G ? tot[g] : 0;
-        int32_t v = c;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int32_t u = __shfl_up(v, o, 64);
-            if (lane >= o) v += u;
-        }
-        if (g <= a.G) base[g] = carry + v - c;
-        carry += __shfl(v, 63, 64);
+    const int per = n / 64 + 1, i0 = threadIdx.x * per, i1 = i0 + per < n ? i0 + per : n;
+    int32_t sum = 0;
+    for (int i = i0; i < i1; i++) sum += in[i];
+    int32_t run = wave_scan(sum) - sum;
+    for (int i = i0; i < i1; i++) {
+        const int32_t v = in[i];
+        out[i] = run;
+        run += v;
     }
+    if (threadIdx.x == 63) out[n] = run;
 }
 
 // Rows of tokens [t0, t1): base[g] is the first row of group g's choices in
 // this run (LDS, advanced here).  Every (group, token) is one bit of an LDS
-// table of 32 W tokens, so a choice's rank among the run's is a population
-// count: rows come out ordered by token whatever the order of execution.
-template <int W>
-__device__ __forceinline__ void route_place(const RouteArgs &a, int64_t t0, int64_t t1, int32_t *base,
-                                            uint32_t (*bits)[W]) {
-    constexpr int H = 4;                      // choices a thread holds between the two passes
-    const int tid = threadIdx.x, nt = blockDim.x;
-    const int step = H * nt / a.kk < 32 * W ? H * nt / a.kk : 32 * W;
-    int tok[H];                               // token (of the pass) of choice h nt + tid
-    {
-        const int dq = nt / a.kk, dr = nt - dq * a.kk;
-        int q = tid / a.kk, r = tid - q * a.kk;
+// table, W words of 32 tokens to a group, so a choice's rank among the run's
+// is a population count: rows come out ordered by token whatever the order of
+// execution.  A thread holds H choices; the first pass's are loaded ahead of
+// the caller's other work.
+//
+// Longer runs (W >= 8) keep the ranks of the words' first bits beside the
+// table (adding up to 16 words for every choice was half of the kernel), and
+// put the rows in order in LDS to write them group by group: a scattered
+// 4-byte store is an L2 request of its own, and at 600018 choices those of src
+// and row_weights took 3 of 13.5 us; in runs of several rows to a group
+// neighbouring lanes share requests.
+template <int H>
+struct Choices {
+    int g[H];
+    float w[H];
+    __device__ __forceinline__ void load(const RouteArgs &a, int64_t s0, int n) {
+        const int tid = threadIdx.x, nt = blockDim.x;
 #pragma unroll
         for (int h = 0; h < H; h++) {
-            tok[h] = q;
-            r += dr;
-            q += dq + (r >= a.kk ? 1 : 0);
-            r -= r >= a.kk ? a.kk : 0;
+            g[h] = -1;
+            w[h] = 0.0f;
+            if (h * nt < n) {
+                const int i = h * nt + tid;
+                const int64_t c = s0 * a.kk + (i < n ? i : 0);
+                const int e = a.experts[c];
+                w[h] = a.weights[c];
+                g[h] = i < n ? e : -1;
+            }
         }
     }
-    for (int64_t s0 = t0; s0 < t1; s0 += step) {
+};
+template <int H, int NT, int W>
+struct PlaceTable {
+    static constexpr bool LONG = W >= 8;
+    static constexpr int GROUPS = W == 16 ? kManyWordsGroups : kMaxGroups;
+    // 16-byte aligned rows of W words
+    __attribute__((aligned(16))) uint32_t bits[GROUPS * W];
+    __attribute__((aligned(16))) uint16_t rank[LONG ? GROUPS * W : 8];   // of a word's first bit
+    int32_t first[LONG ? GROUPS + 1 : 1];                               // of a group, in the order of rows
+    int32_t row[LONG ? H * NT : 1], token[LONG ? H * NT : 1];
+    float weight[LONG ? H * NT : 1];
+    // tokens of one pass: as many as the threads hold choices of and the table has bits for
+    __device__ static __forceinline__ int step(const RouteArgs &a) {
+        const int held = H * NT / a.kk;
+        return held < 32 * W ? held : 32 * W;
+    }
+    __device__ __forceinline__ void clear(const RouteArgs &a) {
+        for (int i = threadIdx.x; i < a.G * W; i += NT) bits[i] = 0;
+    }
+};
+// The table has been cleared, and a barrier passed since.
+template <int H, int NT, int W>
+__device__ __forceinline__ void route_place(const RouteArgs &a, int64_t t0, int64_t t1, int32_t *base,
+                                            PlaceTable<H, NT, W> &tab, Choices<H> &c) {
+    constexpr bool LONG = W >= 8;
+    const int tid = threadIdx.x;
+    const int step = tab.step(a);
+    const int dq = NT / a.kk, dr = NT - dq * a.kk;
+    for (int64_t s0 = t0;;) {
         const int n = (int)(t1 - s0 < step ? t1 - s0 : step) * a.kk;
-        int g[H];
-        float w[H];
+        int tok[H];                                  // token (of the pass) of choice h NT + tid
+        {
+            int t = tid / a.kk, r = tid - t * a.kk;
 #pragma unroll
-        for (int h = 0; h < H; h++) {
-            const int i = h * nt + tid;
-            g[h] = i < n ? a.experts[s0 * a.kk + i] : -1;
-            w[h] = i < n ? a.weights[s0 * a.kk + i] : 0.0f;
-        }
-        for (int i = tid; i < a.G * W; i += nt) bits[0][i] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < H; h++) {
-            if (g[h] >= 0) atomicOr(&bits[g[h]][tok[h] >> 5], 1u << (tok[h] & 31));
+            for (int h = 0; h < H; h++) {
+                tok[h] = t;
+                if (c.g[h] >= 0) atomicOr(&tab.bits[c.g[h] * W + (t >> 5)], 1u << (t & 31));
+                t += dq + (r + dr >= a.kk ? 1 : 0);
+                r += dr - (r + dr >= a.kk ? a.kk : 0);
+            }
         }
         __syncthreads();
+        if constexpr (LONG) {
+            for (int g = tid; g < a.G; g += NT) {
+                uint32_t k = 0;
 #pragma unroll
-        for (int h = 0; h < H; h++) {
-            const int i = h * nt + tid, t = tok[h];
-            int32_t p = -1;
-            if (g[h] >= 0) {
-                p = base[g[h]];
+                for (int x = 0; x < W; x += 8) {
+                    const uint4 lo = *reinterpret_cast<const uint4 *>(tab.bits + g * W + x);
+                    const uint4 hi = *reinterpret_cast<const uint4 *>(tab.bits + g * W + x + 4);
+                    const uint32_t b[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    uint32_t r[4];
 #pragma unroll
-                for (int x = 0; x < W; x++) {
-                    const uint32_t b = bits[g[h]][x];
-                    p += __popc(x < t >> 5 ? b : x == t >> 5 ? b & ((1u << (t & 31)) - 1u) : 0u);
+                    for (int y = 0; y < 8; y += 2) {
+                        const uint32_t k1 = k + __popc(b[y]);
+                        r[y / 2] = k | (k1 << 16);
+                        k = k1 + __popc(b[y + 1]);
+                    }
+                    *reinterpret_cast<uint4 *>(tab.rank + g * W + x) = make_uint4(r[0], r[1], r[2], r[3]);
                 }
-                a.src[p] = (int32_t)(s0 + t);
-                a.row_weights[p] = w[h];
+                tab.first[g] = (int32_t)k;
+            }
+            __syncthreads();
+            exclusive_scan(tab.first, tab.first, a.G);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int h = 0; h < H; h++) {
+            const int i = h * NT + tid, g = c.g[h], t = tok[h];
+            int32_t p = -1;
+            if (g >= 0) {
+                const uint32_t *b = tab.bits + g * W;
+                int rank = __popc(b[t >> 5] & ((1u << (t & 31)) - 1u));
+                if constexpr (LONG) {
+                    rank += tab.rank[g * W + (t >> 5)];
+                } else {
+                    for (int x = 0; x < W - 1; x++) rank += x < t >> 5 ? __popc(b[x]) : 0;
+                }
+                p = base[g] + rank;
+                if constexpr (LONG) {
+                    const int slot = tab.first[g] + rank;
+                    tab.row[slot] = p;
+                    tab.token[slot] = (int32_t)(s0 + t);
+                    tab.weight[slot] = c.w[h];
+                } else {
+                    a.src[p] = (int32_t)(s0 + t);
+                    a.row_weights[p] = c.w[h];
+                }
             }
             if (i < n) a.pos[s0 * a.kk + i] = p;
         }
-        if (s0 + step >= t1) return;
-        __syncthreads();
-        for (int i = tid; i < a.G; i += nt) {
-#pragma unroll
-            for (int x = 0; x < W; x++) base[i] += __popc(bits[i][x]);
+        const bool more = s0 + step < t1;
+        if (more) c.load(a, s0 + step, (int)(t1 - s0 - step < step ? t1 - s0 - step : step) * a.kk);
+        if constexpr (LONG) {
+            __syncthreads();
+            for (int i = tid; i < tab.first[a.G]; i += NT) {
+                const int32_t p = tab.row[i];
+                a.src[p] = tab.token[i];
+                a.row_weights[p] = tab.weight[i];
+            }
         }
+        if (!more) return;
+        s0 += step;
+        __syncthreads();
+        for (int i = tid; i < a.G; i += NT)
+            for (int x = 0; x < W; x++) base[i] += __popc(tab.bits[i * W + x]);
+        __syncthreads();
+        tab.clear(a);
         __syncthreads();
     }
 }
@@ -478,98 +604,145 @@ __device__ __forceinline__ void route_counts(const RouteArgs &a, const int32_t *
 // here, by its one workgroup (ONE).
 template <typename T, int L, int V, int N, int BT, bool ONE, bool VEC>
 __global__ __launch_bounds__(BT) void k_route_select(RouteArgs a) {
-    constexpr int WORDS = kOneWorkgroupTokens / 32;
-    constexpr int PSUM = kSumRows<L, BT> * L * V, BITS = ONE ? (L * V + kMaxShared) * WORDS : 0;
     __shared__ int32_t hist[L * V + kMaxShared + 1];
-    __shared__ __attribute__((aligned(16))) uint32_t buf[PSUM > BITS ? PSUM : BITS];
+    __shared__ __attribute__((aligned(16))) float psum[kSumRows<L, BT> * L * V];
     const int tid = threadIdx.x;
-    float *psum = reinterpret_cast<float *>(buf);
     const int64_t t0 = (int64_t)blockIdx.x * a.CT, t1 = t0 + a.CT < a.T ? t0 + a.CT : a.T;
     route_select<T, L, V, N, BT, VEC>(a, t0, t1, hist, psum);
     if constexpr (ONE) {
+        constexpr int H = 4;
         __shared__ int32_t base[L * V + kMaxShared + 1];
+        __shared__ PlaceTable<H, BT, kOneWorkgroupTokens / 32> tab;
+        Choices<H> c;
+        const int step = tab.step(a);
+        c.load(a, 0, (int)(a.T < step ? a.T : step) * a.kk);
+        tab.clear(a);
         if (a.prob_sum) {
             for (int e = tid; e < a.E; e += BT) a.prob_sum[e] = psum[e];
             if (tid < 64) route_loss(a, hist, psum);
         }
-        route_starts(a, hist, base);
+        exclusive_scan(hist, base, a.G);
         __syncthreads();
         route_counts(a, hist, base);
         const int64_t used = base[a.G];
         __syncthreads();
-        route_place<WORDS>(a, 0, a.T, base, reinterpret_cast<uint32_t(*)[WORDS]>(buf));
+        route_place<H, BT>(a, 0, a.T, base, tab, c);
         route_tail(a, used, tid, BT);
     } else {
-        for (int i = tid; i < a.ldh; i += BT) a.hist[(int64_t)blockIdx.x * a.ldh + i] = i <= a.G ? hist[i] : 0;
+        for (int i = tid; i < a.ldh; i += BT) {
+            const int h = i <= a.G ? hist[i] : 0;
+            if (a.CT > 255)
+                reinterpret_cast<uint16_t *>(a.hist)[((int64_t)(i / 8) * a.nwg + blockIdx.x) * 8 + i % 8] = (uint16_t)h;
+            else
+                reinterpret_cast<uint8_t *>(a.hist)[((int64_t)(i / 16) * a.nwg + blockIdx.x) * 16 + i % 16] = (uint8_t)h;
+        }
         if (a.prob_sum)
             for (int e = tid; e < a.lde; e += BT)
                 a.part[(int64_t)blockIdx.x * a.lde + e] = e < a.E ? psum[e] : 0.0f;
     }
 }
 
-// Column sums of an [n, ld] array by one workgroup, four columns and every
-// parts-th row to a thread with eight rows in flight: f(w, v) sees each
-// 16-byte piece; `quads` = ld / 4.
-template <typename V4, typename F>
-__device__ __forceinline__ void column_pieces(const V4 *__restrict__ x, int n, int quads, int part, int parts, int q,
-                                              F f) {
-    int w = part;
-    for (; w + 7 * parts < n; w += 8 * parts) {
-        V4 v[8];
+// Sums over all runs, and over the runs before run b, of the histograms'
+// columns into tot and before (LDS [ldh]).  A row of 16 lanes takes a piece, a
+// lane every 16th run with 16 in flight (a batch of 256 runs and up to 512
+// bytes of counts is one round trip), and the lanes are added by DPP; adding
+// partial sums by LDS atomics took twice the time of everything else here.
+// u8 counts are added as pairs of 16 bits: a column's total is at most
+// T <= 256 * 255.
+template <typename HT, int NT>
+__device__ __forceinline__ void route_totals(const RouteArgs &a, int b, int32_t *tot, int32_t *before) {
+    constexpr int P = 16 / sizeof(HT), U = 16;
+    const int lane = threadIdx.x & 15;
+    for (int q = threadIdx.x >> 4; q < a.ldh / P; q += NT / 16) {
+        const uint4 *x = reinterpret_cast<const uint4 *>(a.hist) + (int64_t)q * a.nwg;
+        uint32_t s[8], sb[8];                    // words of two 16-bit counts (u8), or counts
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = x[(int64_t)(w + i * parts) * quads + q];
+        for (int i = 0; i < 8; i++) s[i] = sb[i] = 0;
+        for (int w0 = lane; w0 < a.nwg; w0 += 16 * U) {
+            uint4 h[U];
 #pragma unroll
-        for (int i = 0; i < 8; i++) f(w + i * parts, v[i]);
+            for (int u = 0; u < U; u++) h[u] = x[w0 + 16 * u < a.nwg ? w0 + 16 * u : 0];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const uint32_t all = w0 + 16 * u < a.nwg ? ~0u : 0u, m = w0 + 16 * u < b ? ~0u : 0u;
+                const uint32_t v[4] = {h[u].x & all, h[u].y & all, h[u].z & all, h[u].w & all};
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const uint32_t even = sizeof(HT) == 1 ? v[i] & 0x00FF00FFu : v[i] & 0xFFFFu;
+                    const uint32_t odd = sizeof(HT) == 1 ? (v[i] >> 8) & 0x00FF00FFu : v[i] >> 16;
+                    s[2 * i] += even;
+                    s[2 * i + 1] += odd;
+                    sb[2 * i] += even & m;
+                    sb[2 * i + 1] += odd & m;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            s[i] = row_sum(s[i]);
+            sb[i] = row_sum(sb[i]);
+        }
+        // every lane has the sums: lane c of the row writes column c
+        if (lane < P) {
+            uint32_t v = 0, vb = 0;
+            const int i = sizeof(HT) == 1 ? 2 * (lane / 4) + lane % 2 : lane;   // u8: byte lane % 4 of word lane / 4
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                v = i == k ? s[k] : v;
+                vb = i == k ? sb[k] : vb;
+            }
+            const int sh = 16 * ((lane % 4) / 2);
+            tot[P * q + lane] = (int32_t)(sizeof(HT) == 1 ? (v >> sh) & 0xFFFFu : v);
+            before[P * q + lane] = (int32_t)(sizeof(HT) == 1 ? (vb >> sh) & 0xFFFFu : vb);
+        }
     }
-    for (; w < n; w += parts) f(w, x[(int64_t)w * quads + q]);
+    __syncthreads();
 }
 
 // Second launch: workgroup b < nwg places the rows of its run; workgroup nwg
 // sums the probabilities.  Every workgroup adds up the histograms of all runs
-// by itself (what precedes its run, and the totals): at most 512 rows of
-// 4 (G + 1) bytes from L2, which is less than a third launch costs.
-__global__ __launch_bounds__(kRouteThreads) void k_route_place(RouteArgs a) {
-    __shared__ int32_t tot[kMaxGroups + 4], before[kMaxGroups + 4], base[kMaxGroups + 1];
-    __shared__ __attribute__((aligned(16))) uint32_t bits[kMaxGroups][kWords];
+// by itself (what precedes its run, and the totals): about 256 rows of G + 1
+// bytes (or 2-byte words) from L2, which is less than a third launch costs.
+template <typename HT, int NT, int W>
+__global__ __launch_bounds__(NT) void k_route_place(RouteArgs a) {
+    constexpr int H = 4;
+    __shared__ int32_t tot[kMaxGroups + 16], before[kMaxGroups + 16], base[kMaxGroups + 1];
+    __shared__ PlaceTable<H, NT, W> tab;
+    __shared__ __attribute__((aligned(16))) float red[4 * NT + 1024];
     const int tid = threadIdx.x, b = blockIdx.x;
-    for (int i = tid; i < a.ldh; i += kRouteThreads) tot[i] = before[i] = 0;
-    __syncthreads();
-    {
-        const int quads = a.ldh / 4, parts = kRouteThreads / quads, part = tid / quads, q = tid % quads;
-        if (part < parts) {
-            int s[4] = {0, 0, 0, 0}, sb[4] = {0, 0, 0, 0};
-            column_pieces(reinterpret_cast<const int4 *>(a.hist), a.nwg, quads, part, parts, q, [&](int w, int4 h) {
-                const int m = w < b ? -1 : 0, v[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    s[i] += v[i];
-                    sb[i] += v[i] & m;
-                }
-            });
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                atomicAdd(&tot[4 * q + i], s[i]);
-                atomicAdd(&before[4 * q + i], sb[i]);
-            }
-        }
+    const int64_t t0 = (int64_t)b * a.CT, t1 = t0 + a.CT < a.T ? t0 + a.CT : a.T;
+    Choices<H> c;
+    if (b < a.nwg) {
+        const int step = tab.step(a);
+        c.load(a, t0, (int)(t1 - t0 < step ? t1 - t0 : step) * a.kk);
+        tab.clear(a);
     }
-    __syncthreads();
+    route_totals<HT, NT>(a, b, tot, before);
     if (b == a.nwg) {                       // the loss's workgroup
-        float *red = reinterpret_cast<float *>(bits);   // [parts][lde], at most 4 floats per thread
-        const int quads = a.lde / 4, parts = kRouteThreads / quads, part = tid / quads, q = tid % quads;
+        // red: [parts][lde], at most 4 floats per thread, then the sums
+        const int quads = a.lde / 4, parts = NT / quads, part = tid / quads, q = tid % quads;
         if (part < parts) {
+            constexpr int U = 4;
+            const float4 *x = reinterpret_cast<const float4 *>(a.part);
             float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            column_pieces(reinterpret_cast<const float4 *>(a.part), a.nwg, quads, part, parts, q, [&](int, float4 v) {
-                s.x += v.x;
-                s.y += v.y;
-                s.z += v.z;
-                s.w += v.w;
-            });
+            for (int w = part; w < a.nwg; w += U * parts) {
+                float4 v[U];
+#pragma unroll
+                for (int u = 0; u < U; u++) v[u] = x[(int64_t)(w + u * parts < a.nwg ? w + u * parts : 0) * quads + q];
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const bool in = w + u * parts < a.nwg;
+                    s.x += in ? v[u].x : 0.0f;
+                    s.y += in ? v[u].y : 0.0f;
+                    s.z += in ? v[u].z : 0.0f;
+                    s.w += in ? v[u].w : 0.0f;
+                }
+            }
             reinterpret_cast<float4 *>(red)[part * quads + q] = s;
         }
         __syncthreads();
-        float *sum = red + 4 * kRouteThreads;
-        for (int e = tid; e < a.E; e += kRouteThreads) {
+        float *sum = red + 4 * NT;
+        for (int e = tid; e < a.E; e += NT) {
             float s = 0.0f;
             for (int w = 0; w < parts; w++) s += red[w * a.lde + e];
             sum[e] = s;
@@ -579,40 +752,40 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(RouteArgs a) {
         if (tid < 64) route_loss(a, tot, sum);
         return;
     }
-    route_starts(a, tot, base);
+    exclusive_scan(tot, base, a.G);   // group starts; base[G] is the rows in use
     __syncthreads();
     const int64_t used = base[a.G];
     if (b == 0) {
         route_counts(a, tot, base);
         __syncthreads();
     }
-    for (int i = tid; i < a.G; i += kRouteThreads) base[i] += before[i];
+    for (int i = tid; i < a.G; i += NT) base[i] += before[i];
     __syncthreads();
-    const int64_t t0 = (int64_t)b * a.CT, t1 = t0 + a.CT < a.T ? t0 + a.CT : a.T;
-    route_place<kWords>(a, t0, t1, base, bits);
-    route_tail(a, used, (int64_t)b * kRouteThreads + tid, (int64_t)a.nwg * kRouteThreads);
+    route_place<H, NT, W>(a, t0, t1, base, tab, c);
+    route_tail(a, used, (int64_t)b * NT + tid, (int64_t)a.nwg * NT);
 }
 
-static int32_t round4(int64_t n) { return (int32_t)((n + 3) / 4 * 4); }
+static int32_t round_up(int64_t n, int64_t m) { return (int32_t)((n + m - 1) / m * m); }
 
-// Runs of whole words of tokens, at most 256 of them once a run is 256 tokens
-// long (its workgroup then has 1024 threads).
+// Runs of whole words of tokens, about one to a compute unit (the placing reads
+// every run's histogram in every workgroup), with counts below 2^16.
 static void route_runs(int64_t T, int32_t &CT, int32_t &nwg) {
-    CT = (int32_t)(((T + 255) / 256 + 31) / 32 * 32);
-    if (T <= kOneWorkgroupTokens) CT = (int32_t)kOneWorkgroupTokens;
+    CT = T <= kOneWorkgroupTokens ? (int32_t)kOneWorkgroupTokens
+                                  : T >= 256 * 65504ll ? 65504 : round_up((T + 255) / 256, 32);
     nwg = (int32_t)((T + CT - 1) / CT);
 }
 
 int64_t route_workspace_bytes(int64_t T, int64_t E, int64_t shared) {
     int32_t CT, nwg;
     route_runs(T, CT, nwg);
-    return nwg == 1 ? 0 : (int64_t)nwg * 4 * (round4(E + shared + 1) + round4(E));
+    return nwg == 1 ? 0 : (int64_t)nwg * ((CT > 255 ? 2 : 1) * round_up(E + shared + 1, 16) + 4 * round_up(E, 4));
 }
 
 template <typename T, int L, int V, int N, bool VEC>
 static void route_launch_few(const RouteArgs &a, hipStream_t s) {
+    constexpr int B = N == 8 && L > 8 && L * V <= 512 ? 512 : 256;
     if (a.nwg == 1) k_route_select<T, L, V, N, 256, true, VEC><<<1, 256, 0, s>>>(a);
-    else k_route_select<T, L, V, N, 256, false, VEC><<<a.nwg, 256, 0, s>>>(a);
+    else k_route_select<T, L, V, N, B, false, VEC><<<a.nwg, B, 0, s>>>(a);
 }
 template <typename T, int L, int V, bool VEC>
 static void route_few(const RouteArgs &a, hipStream_t s) {
@@ -624,13 +797,13 @@ template <typename T, bool VEC>
 static void route_few_experts(const RouteArgs &a, hipStream_t s) {
     constexpr int Q = kPiece<T>;
     if (a.E <= 64) route_few<T, 64 / Q, Q, VEC>(a, s);
-    else if (a.E <= 128) route_few<T, 16, 8, VEC>(a, s);
+    else if (a.E <= 128) route_few<T, 8, 16, VEC>(a, s);
     else if (a.E <= 256) route_few<T, 16, 16, VEC>(a, s);
     else if (a.E <= 512) route_few<T, 32, 16, VEC>(a, s);
     else route_few<T, 32, 32, VEC>(a, s);
 }
 
-constexpr int kManyThreads = 512;
+constexpr int kManyThreads = 768;
 template <typename T>
 static void route_dispatch(const RouteArgs &a, bool vec, hipStream_t s) {
     if (a.T >= kManyTokens && a.k <= 8 && a.E <= 256 && vec) {
@@ -643,7 +816,12 @@ static void route_dispatch(const RouteArgs &a, bool vec, hipStream_t s) {
     } else {
         route_few_experts<T, false>(a, s);
     }
-    if (a.nwg > 1) k_route_place<<<a.nwg + (a.prob_sum ? 1 : 0), kRouteThreads, 0, s>>>(a);
+    if (a.nwg == 1) return;
+    const unsigned grid = (unsigned)(a.nwg + (a.prob_sum ? 1 : 0));
+    if (a.CT > 255 && a.G <= kManyWordsGroups) k_route_place<uint16_t, 1024, 16><<<grid, 1024, 0, s>>>(a);
+    else if (a.CT > 255) k_route_place<uint16_t, 1024, 8><<<grid, 1024, 0, s>>>(a);
+    else if (a.CT > 32) k_route_place<uint8_t, 512, 8><<<grid, 512, 0, s>>>(a);
+    else k_route_place<uint8_t, 512, 1><<<grid, 512, 0, s>>>(a);
 }
 
 // Whole 16-byte pieces: pointers are 16-byte aligned (checked at the C ABI).
@@ -664,10 +842,11 @@ hipError_t launch_route(const void *logits, int dtype, int64_t T, int64_t E, int
     a.experts = experts; a.counts = counts; a.src = src; a.pos = pos;
     a.weights = weights; a.row_weights = row_weights; a.prob_sum = prob_sum; a.loss = loss; a.off = off;
     route_runs(T, a.CT, a.nwg);
-    a.ldh = round4(E + shared + 1);
-    a.lde = round4(E);
-    a.hist = reinterpret_cast<int32_t *>(workspace);
-    a.part = reinterpret_cast<float *>(a.hist + (int64_t)a.nwg * a.ldh);
+    a.ldh = round_up(E + shared + 1, 16);
+    a.lde = round_up(E, 4);
+    a.hist = workspace;
+    a.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) +
+                                       (int64_t)a.nwg * a.ldh * (a.CT > 255 ? 2 : 1));
     if (dtype == BSP_DTYPE_BF16) route_dispatch<uint16_t>(a, vec, s);
     else route_dispatch<float>(a, vec, s);
     return hipGetLastError();
@@ -700,52 +879,50 @@ template <typename T, int L, int V, bool VEC>
 __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
     constexpr int KS = 32 / L;                // choices per lane, k <= 32
     const int tid = threadIdx.x, lane = tid & (L - 1), grp = tid / L;
-    float f[V], coef = 0.0f, rn = 0.0f;
-    if (a.d_loss) {
-        const int32_t n = a.counts[a.G];
-        rn = 1.0f / (n > 0 ? (float)n : 1.0f);
-        coef = *a.d_loss * ((float)a.E / (float)a.k) * rn;
-    }
+    const int32_t n = a.counts[a.G];
+    const float rn = 1.0f / (n > 0 ? (float)n : 1.0f);
+    const float coef = a.d_loss ? *a.d_loss * ((float)a.E / (float)a.k) * rn : 0.0f;
+    float f[V];
 #pragma unroll
     for (int i = 0; i < V; i++) {
         const int e = expert_of<T, L>(lane, i);
-        f[i] = a.d_loss && e < a.E ? (float)a.counts[e] * rn : 0.0f;
+        f[i] = (float)a.counts[e < a.E ? e : 0] * rn;
     }
     for (int64_t t = (int64_t)blockIdx.x * (256 / L) + grp; t < a.T; t += (int64_t)gridDim.x * (256 / L)) {
         const T *in = reinterpret_cast<const T *>(a.logits) + t * a.ldl;
         T *out = reinterpret_cast<T *>(a.d_logits) + t * a.ldd;
-        float v[V];
-        if (a.mask && !a.mask[t]) {
-#pragma unroll
-            for (int i = 0; i < V; i++) v[i] = 0.0f;
-            store_logits<T, L, V, VEC>(out, lane, a.E, v);
-            continue;
-        }
-        load_logits<T, L, V, VEC>(in, lane, a.E, v);
-        int ex[KS];
+        RowLoad<T, L, V, VEC> rows;
+        rows.load(in, lane, a.E);
+        const bool keep = !a.mask || a.mask[t];
+        // choice j = q L + lane: expert, then its logit, count and gradient
+        int ex[KS], cnt[KS];
         float x[KS], dw[KS];
 #pragma unroll
         for (int q = 0; q < KS; q++) {
-            const int j = q * L + lane;
             ex[q] = -1;
             x[q] = -INFINITY;
             dw[q] = 0.0f;
-            if (a.d_weights && j < a.k) {
-                const int e = a.experts[t * a.kk + j];
-                const int32_t r = a.pos[t * a.kk + j];
-                if (e >= 0 && e < a.E && r >= 0 && r < a.rows) {
-                    ex[q] = e;
-                    x[q] = elem(in + e);
-                    dw[q] = a.d_weights[r];
-                }
+            cnt[q] = 0;
+            if (a.d_weights && q * L < a.k) {
+                const int j = q * L + lane;
+                const int64_t c = t * a.kk + (j < a.k ? j : 0);
+                const int e = a.experts[c], r = a.pos[c];
+                const bool ok = j < a.k && keep && e >= 0 && e < a.E && r >= 0 && r < a.rows;
+                const float l = elem(in + (ok ? e : 0)), g = a.d_weights[ok ? r : 0];
+                cnt[q] = a.counts[ok ? e : 0];
+                ex[q] = ok ? e : -1;
+                x[q] = ok ? l : -INFINITY;
+                dw[q] = ok ? g : 0.0f;
             }
         }
+        float v[V];
+        rows.get(lane, a.E, keep, v);
         float m = v[0];
 #pragma unroll
         for (int i = 1; i < V; i++) m = fmaxf(m, v[i]);
         m = group_max<L>(m);
         m = m > -INFINITY ? m : 0.0f;
-        const float sum = exp_sum<L>(v, m), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float sum = exp_sum<L>(v, m), inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
         float dot = 0.0f, ps = 0.0f, pd = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; i++) dot = fmaf(v[i], f[i], dot);
@@ -759,7 +936,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
         ps = group_sum<L>(ps);
         pd = group_sum<L>(pd);
         // renormalised: chosen p / ps; else p itself, whose sum of p dw every expert feels
-        const float scale = a.norm ? (ps > 0.0f ? 1.0f / ps : 0.0f) : inv;
+        const float scale = a.norm ? (ps > 0.0f ? __builtin_amdgcn_rcpf(ps) : 0.0f) : inv;
         const float c1 = coef * inv, c2 = c1 * dot + (a.norm ? 0.0f : inv * inv * pd);
 #pragma unroll
         for (int i = 0; i < V; i++) v[i] *= fmaf(c1, f[i], -c2);
@@ -769,7 +946,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
 #pragma unroll
         for (int q = 0; q < KS; q++)
             if (ex[q] >= 0) {
-                const float fe = a.d_loss ? (float)a.counts[ex[q]] * rn : 0.0f;
+                const float fe = (float)cnt[q] * rn;
                 put(out + ex[q], x[q] * (fmaf(c1, fe, -c2) + scale * (dw[q] - (a.norm ? pd * scale : 0.0f))));
             }
     }

@@ -447,8 +447,8 @@ bsp_status bsp_swiglu_quantize(const void *h13, int in_dtype, int64_t R, int64_t
  *   T, E     1 <= E <= 1024; k experts per token, 1 <= k <= min(E, 32);
  *            `shared` (0..64) further groups that every routed token joins with
  *            weight 1.  kk = k + shared, G = E + shared, T * kk < 2^31.
- *   token_mask  device u8 [T] or NULL: 0 = padding token; its logits are not
- *            read and it takes no row.  A token is routed when its mask is not
+ *   token_mask  device u8 [T] or NULL: 0 = padding token; its logits may hold
+ *            anything and it takes no row.  A token is routed when its mask is not
  *            0 and some logit is above -inf.
  *   flags    0 or BSP_ROUTE_NORM
  *   experts  device int32 [T, kk] (out): the k largest logits in decreasing

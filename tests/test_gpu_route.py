@@ -90,7 +90,7 @@ def test_route_forward_and_backward(T, E, k, shared, dtype, norm, kind, masked, 
     if masked:
         mask = rng.random(T) >= masked
         maskd = to_dev(mask)
-        xd[~maskd] = float("nan")              # a padding token's logits are not read
+        xd[~maskd] = float("nan")              # a padding token's logits may hold anything
     want = ref.route(x, k, norm, shared, mask)
     got = ops.moe_route(xd, k, norm=norm, shared=shared, token_mask=maskd, aux=True)
     check_forward(got, want, x, k, mask)
