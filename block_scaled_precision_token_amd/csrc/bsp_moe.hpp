@@ -44,28 +44,60 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, b2));
 }
 
-// Eight consecutive values (16-byte aligned) as f32, and back (bf16: nearest even).
-__device__ __forceinline__ void ld8(const float *p, float (&v)[8]) {
-    const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+// Loads and stores of 16 and 8 bytes; NT: nontemporal (data used once).
+typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32v2 __attribute__((ext_vector_type(2)));
+template <bool NT>
+__device__ __forceinline__ u32v4 ld4w(const void *p) {
+    const u32v4 *q = reinterpret_cast<const u32v4 *>(p);
+    return NT ? __builtin_nontemporal_load(q) : *q;
 }
-__device__ __forceinline__ void ld8(const uint16_t *p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+template <bool NT>
+__device__ __forceinline__ void st4w(void *p, u32v4 v) {
+    u32v4 *q = reinterpret_cast<u32v4 *>(p);
+    if (NT) __builtin_nontemporal_store(v, q);
+    else *q = v;
+}
+template <bool NT>
+__device__ __forceinline__ uint2 ld2(const void *p) {
+    const u32v2 *q = reinterpret_cast<const u32v2 *>(p);
+    const u32v2 v = NT ? __builtin_nontemporal_load(q) : *q;
+    return make_uint2(v.x, v.y);
+}
+template <bool NT>
+__device__ __forceinline__ void st2(void *p, uint2 v) {
+    u32v2 *q = reinterpret_cast<u32v2 *>(p);
+    if (NT) __builtin_nontemporal_store((u32v2){v.x, v.y}, q);
+    else *q = (u32v2){v.x, v.y};
+}
+
+// Eight consecutive values (16-byte aligned) as f32, and back (bf16: nearest even).
+template <bool NT>
+__device__ __forceinline__ void ld8(const float *p, float (&v)[8]) {
+    const u32v4 x = ld4w<NT>(p), y = ld4w<NT>(p + 4);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        v[2 * i] = bf16_lo(w[i]);
-        v[2 * i + 1] = bf16_hi(w[i]);
+        v[i] = __uint_as_float(x[i]);
+        v[4 + i] = __uint_as_float(y[i]);
     }
 }
-__device__ __forceinline__ void st8(float *p, const float (&v)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+template <bool NT>
+__device__ __forceinline__ void ld8(const uint16_t *p, float (&v)[8]) {
+    const u32v4 u = ld4w<NT>(p);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        v[2 * i] = bf16_lo(u[i]);
+        v[2 * i + 1] = bf16_hi(u[i]);
+    }
 }
+template <bool NT>
+__device__ __forceinline__ void st8(float *p, const float (&v)[8]) {
+    st4w<NT>(p, (u32v4){__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+    st4w<NT>(p + 4, (u32v4){__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
+}
+template <bool NT>
 __device__ __forceinline__ void st8(uint16_t *p, const float (&v)[8]) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
-                                               bf16x2(v[6], v[7]));
+    st4w<NT>(p, (u32v4){bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])});
 }
 
 }  // namespace bsp
