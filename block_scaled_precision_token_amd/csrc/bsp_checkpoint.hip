@@ -14,12 +14,14 @@
 // contiguous run, and a block of 32 values lies on 32 / VE neighbouring lanes:
 // its maximum is two or three DPP steps.
 //
-// Cache policy, which decides between 5.1 and 6.8 TB/s here: inputs are loaded
-// nontemporally (read once; forward 65536 x 768: 74.6 -> 62 us), and of the
-// outputs the larger part is stored nontemporally -- dh13, and the checkpoint,
-// which nobody reads before the backward pass -- while h, the next product's
-// operand, stays cached.  Backward 65536 x 768: all cached 99.6 us, all
-// nontemporal 86, this split 77 (6.6 TB/s); 36864 x 2048: 138, 130, 113.
+// Cache policy, which decides between 5.1 and 6.7 TB/s here.  Inputs are loaded
+// nontemporally (read once; forward 65536 x 768 bf16 74.6 -> 62 us), and of the
+// outputs the larger part is stored nontemporally: dh13, and the checkpoint,
+// which nobody reads before the backward pass.  h, the next product's operand,
+// stays in the 256 MiB last-level cache where it fits there beside what that
+// product reads, and is nontemporal past 128 MiB, where it would push itself
+// out.  Backward 65536 x 768 (h 96 MiB): all cached 99.6 us, all nontemporal 86,
+// h cached 76 (6.6 TB/s); 36864 x 2048 (h 144 MiB): 138, 130, 135.
 // Keeping more than one piece per lane in flight changed nothing for bf16 and
 // cost f32 3 to 10 %.
 #include <type_traits>
@@ -49,11 +51,14 @@ __device__ __forceinline__ void st_nt(float *p, const float (&v)[4]) {
     st4w<true>(p, (u32v4){__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
 }
 __device__ __forceinline__ void st_nt(uint16_t *p, const float (&v)[8]) { st8<true>(p, v); }
-// h: bf16, cached
+// h: bf16
+template <bool NT>
 __device__ __forceinline__ void st_h(uint16_t *p, const float (&v)[4]) {
-    st2<false>(p, make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3])));
+    st2<NT>(p, make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3])));
 }
-__device__ __forceinline__ void st_h(uint16_t *p, const float (&v)[8]) { st8<false>(p, v); }
+template <bool NT>
+__device__ __forceinline__ void st_h(uint16_t *p, const float (&v)[8]) { st8<NT>(p, v); }
+constexpr int64_t kCachedH = 128ll << 20;   // bytes of h kept in the last-level cache
 
 // The E4M3 codes of VE values.
 template <int VE>
@@ -129,7 +134,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }  // namespace
 
 // LPR lanes to a row.
-template <typename T, int LPR>
+template <typename T, int LPR, bool HNT>
 __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt(const T *__restrict__ h13, int64_t R, int64_t I,
                                                      const float *__restrict__ row_weights,
                                                      const int64_t *__restrict__ n_rows, uint16_t *__restrict__ h_out,
@@ -162,7 +167,7 @@ __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt(const T *__restrict__ h1
         }
 #pragma unroll
         for (int i = 0; i < VE; i++) h[i] = w * (g[i] * sigmoid(g[i]) * u[i]);
-        if (h_out) st_h(h_out + r * I + c, h);
+        if (h_out) st_h<HNT>(h_out + r * I + c, h);
         if (codes) {
 #pragma unroll
             for (int i = 0; i < VE; i++) h[i] = __uint_as_float(bf16x2(0.0f, h[i]) & 0xFFFF0000u);
@@ -174,7 +179,7 @@ __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt(const T *__restrict__ h1
     }
 }
 
-template <typename T, int LPR>
+template <typename T, int LPR, bool HNT>
 __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt_bwd(const T *__restrict__ dh, int64_t R, int64_t I,
                                                          const uint8_t *__restrict__ ckpt_codes,
                                                          const uint8_t *__restrict__ ckpt_scales,
@@ -212,7 +217,7 @@ __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt_bwd(const T *__restrict_
         }
         st_nt(dh13 + at, dg);
         st_nt(dh13 + at + I, du);
-        if (h_out) st_h(h_out + r * I + c, h);
+        if (h_out) st_h<HNT>(h_out + r * I + c, h);
     }
     if (d_row_weights) {
         dw = lanes_sum<LPR>(dw);
@@ -224,21 +229,25 @@ __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt_bwd(const T *__restrict_
 // time (200000 x 160 bf16, 20 pieces, backward: 53 us with 32 lanes, 84 with 64
 // and 80 with 8, the fewest idle).
 template <typename T, typename F>
-static void with_lanes(int64_t I, F f) {
+static void with_lanes(int64_t R, int64_t I, F f) {
     const int64_t n = I / kVE<T>;
-    if (n > 32) f(std::integral_constant<int, 64>());
-    else if (n > 16) f(std::integral_constant<int, 32>());
-    else if (n > 8) f(std::integral_constant<int, 16>());
-    else f(std::integral_constant<int, 8>());
+    auto lanes = [&](auto nt) {
+        if (n > 32) f(std::integral_constant<int, 64>(), nt);
+        else if (n > 16) f(std::integral_constant<int, 32>(), nt);
+        else if (n > 8) f(std::integral_constant<int, 16>(), nt);
+        else f(std::integral_constant<int, 8>(), nt);
+    };
+    if (R * I * 2 > kCachedH) lanes(std::true_type());
+    else lanes(std::false_type());
 }
 
 template <typename T>
 static void ckpt_launch(const void *h13, int64_t R, int64_t I, const float *row_weights, const int64_t *n_rows,
                         uint16_t *h_out, uint8_t *codes, uint8_t *scales, uint8_t *ckpt_codes, uint8_t *ckpt_scales,
                         hipStream_t s) {
-    with_lanes<T>(I, [&](auto l) {
+    with_lanes<T>(R, I, [&](auto l, auto nt) {
         constexpr int LPR = decltype(l)::value, RW = 256 / LPR;
-        k_swiglu_ckpt<T, LPR><<<(unsigned)((R + RW - 1) / RW), 256, 0, s>>>(
+        k_swiglu_ckpt<T, LPR, decltype(nt)::value><<<(unsigned)((R + RW - 1) / RW), 256, 0, s>>>(
             reinterpret_cast<const T *>(h13), R, I, row_weights, n_rows, h_out, codes, scales, ckpt_codes, ckpt_scales);
     });
 }
@@ -247,9 +256,9 @@ template <typename T>
 static void ckpt_bwd_launch(const void *dh, int64_t R, int64_t I, const uint8_t *ckpt_codes,
                             const uint8_t *ckpt_scales, const float *row_weights, const int64_t *n_rows, void *dh13,
                             uint16_t *h_out, float *d_row_weights, hipStream_t s) {
-    with_lanes<T>(I, [&](auto l) {
+    with_lanes<T>(R, I, [&](auto l, auto nt) {
         constexpr int LPR = decltype(l)::value, RW = 256 / LPR;
-        k_swiglu_ckpt_bwd<T, LPR><<<(unsigned)((R + RW - 1) / RW), 256, 0, s>>>(
+        k_swiglu_ckpt_bwd<T, LPR, decltype(nt)::value><<<(unsigned)((R + RW - 1) / RW), 256, 0, s>>>(
             reinterpret_cast<const T *>(dh), R, I, ckpt_codes, ckpt_scales, row_weights, n_rows,
             reinterpret_cast<T *>(dh13), h_out, d_row_weights);
     });
