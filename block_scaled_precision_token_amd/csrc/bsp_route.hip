@@ -15,7 +15,7 @@ namespace bsp {
 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr int64_t kManyTokens = 32768;
-constexpr int64_t kBwdWorkgroups = 1024;
+constexpr int64_t kBwdWorkgroups = 768;   // three to a compute unit, as the registers of the widest form allow
 constexpr int64_t kOneWorkgroupTokens = 64;
 constexpr int kMaxShared = 64;
 constexpr int kMaxGroups = 1024 + kMaxShared;

@@ -287,7 +287,8 @@ bsp_status bsp_requant_transpose_sr_batched(const uint8_t *codes, const uint8_t 
  *     a_codes/a_scales  device A [a_rows, K] quantized along K
  *     a_outer   device f32 [a_rows] (NVFP4 per-token scales; NULL for MXFP8)
  *     a_gather  device int32 [M] or NULL (then a_rows == M)
- *     group_offsets  device int64 [G+1]: rows of C per group, off[G] == M
+ *     group_offsets  device int64 [G+1]: rows of C per group, off[G] <= M;
+ *               rows of C from off[G] on are left untouched
  *     M, N, K   rows of C, columns of C, reduction length (K % 32 == 0 for
  *               both formats: operand rows are fetched in 16-byte pieces);
  *               sizes below 2^31, and each operand's codes (A, one expert
@@ -386,12 +387,12 @@ bsp_status bsp_moe_grouped_gemm_blockscaled_noalloc(int fmt, int mode, const uin
  *              index outside [0, src_rows) reads as zeros
  *     DGRAD: N % 8 == 0
  *     C        device [M, ldc] of c_dtype; group_offsets: rows of C per
- *              group, off[G] == M
+ *              group, off[G] <= M (rows from off[G] on are left untouched)
  * WGRAD, reducing over the rows of each group:
  *   C_g[m, n] = sum_{r in [off[g], off[g+1])} A[r, m] * B[t, n],
  *   t = gather[r] (or r): dW_e = dY_e^T * X_e with the routed rows of X read
  *   through the routing map, and no transposed copies
- *     a        device bf16 [K, lda >= M] (K = off[G], rows in grouped order)
+ *     a        device bf16 [K, lda >= M] (K >= off[G], rows in grouped order)
  *     b        device bf16 [src_rows, ldb >= N]
  *     gather   device int32 [K] or NULL (then src_rows == K); an index
  *              outside [0, src_rows) contributes nothing
