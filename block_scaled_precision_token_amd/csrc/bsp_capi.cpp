@@ -396,9 +396,9 @@ inline bool known_dtype(int d) { return d == BSP_DTYPE_F32 || d == BSP_DTYPE_BF1
 
 }  // namespace
 
-BSP_EXPORT size_t bsp_moe_route_workspace_size(int64_t T, int64_t E, int64_t shared) {
-    if (route_shape(T, E, E, 1, shared) != BSP_OK) return 0;
-    return (size_t)bsp::route_workspace_bytes(T, E, shared);
+BSP_EXPORT size_t bsp_moe_route_workspace_size(int64_t T, int64_t E, int64_t k, int64_t shared) {
+    if (route_shape(T, E, E, k, shared) != BSP_OK) return 0;
+    return (size_t)bsp::route_workspace_bytes(T, E, k, shared);
 }
 
 BSP_EXPORT bsp_status bsp_moe_route(const void *logits, int dtype, int64_t T, int64_t E, int64_t ldl,
@@ -412,7 +412,7 @@ BSP_EXPORT bsp_status bsp_moe_route(const void *logits, int dtype, int64_t T, in
     if (!known_dtype(dtype) || (flags & ~BSP_ROUTE_NORM)) return BSP_ERR_INVALID_ARG;
     const bsp_status shape = route_shape(T, E, ldl, k, shared);
     if (shape != BSP_OK) return shape;
-    const size_t need = bsp_moe_route_workspace_size(T, E, shared);
+    const size_t need = bsp_moe_route_workspace_size(T, E, k, shared);
     if (need > 0 && (!workspace || ws_bytes < need)) return BSP_ERR_WORKSPACE;
     if (!aligned16(logits) || !aligned16_or_null(token_mask) || !aligned16(experts) || !aligned16(weights) ||
         !aligned16(counts) || !aligned16(group_offsets) || !aligned16(src) || !aligned16(pos) ||

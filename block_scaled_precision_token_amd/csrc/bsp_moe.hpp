@@ -8,7 +8,7 @@
 
 namespace bsp {
 
-int64_t route_workspace_bytes(int64_t T, int64_t E, int64_t shared);
+int64_t route_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t shared);
 hipError_t launch_route(const void *logits, int dtype, int64_t T, int64_t E, int64_t ldl, const uint8_t *mask,
                         int64_t k, int64_t shared, int32_t *experts, float *weights, int32_t *counts, int64_t *off,
                         int32_t *src, int32_t *pos, float *row_weights, float *prob_sum, float *loss, bool norm,

@@ -14,12 +14,15 @@
 namespace bsp {
 
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr int64_t kManyTokens = 32768;
+constexpr int64_t kManyTokens = 16384;
 constexpr int64_t kBwdWorkgroups = 768;   // three to a compute unit, as the registers of the widest form allow
-constexpr int64_t kOneWorkgroupTokens = 64;
+// Batches that one workgroup finishes in one launch: of 256 threads, or of 1024
+// for up to 256 experts and k <= 8 (128 tokens, 128 experts: 10.5 us a call
+// instead of 15.3 with two launches; 256 tokens: 14.5, and 24 with 256 experts).
+constexpr int64_t kOneSmallTokens = 64, kOneLargeTokens = 128;
 constexpr int kMaxShared = 64;
 constexpr int kMaxGroups = 1024 + kMaxShared;
-constexpr int kManyWordsGroups = kMaxGroups / 2;   // groups of the widest rank table
+constexpr int kFewGroups = kMaxGroups / 2;   // placing: groups of the smaller rank table
 
 // Lane exchanges within a row of 16 by DPP.  A token's L lanes (4, 8, 16 or 32)
 // reduce over mirror(16), mirror(8), xor 2, xor 1, each step joining two
@@ -476,10 +479,9 @@ struct Choices {
         }
     }
 };
-template <int H, int NT, int W>
+template <int H, int NT, int W, int GROUPS>
 struct PlaceTable {
     static constexpr bool LONG = W >= 8;
-    static constexpr int GROUPS = W == 16 ? kManyWordsGroups : kMaxGroups;
     // 16-byte aligned rows of W words
     __attribute__((aligned(16))) uint32_t bits[GROUPS * W];
     __attribute__((aligned(16))) uint16_t rank[LONG ? GROUPS * W : 8];   // of a word's first bit
@@ -496,9 +498,9 @@ struct PlaceTable {
     }
 };
 // The table has been cleared, and a barrier passed since.
-template <int H, int NT, int W>
+template <int H, int NT, int W, int GROUPS>
 __device__ __forceinline__ void route_place(const RouteArgs &a, int64_t t0, int64_t t1, int32_t *base,
-                                            PlaceTable<H, NT, W> &tab, Choices<H> &c) {
+                                            PlaceTable<H, NT, W, GROUPS> &tab, Choices<H> &c) {
     constexpr bool LONG = W >= 8;
     const int tid = threadIdx.x;
     const int step = tab.step(a);
@@ -600,19 +602,19 @@ __device__ __forceinline__ void route_counts(const RouteArgs &a, const int32_t *
     }
 }
 
-// First launch.  A batch of one run (T <= kOneWorkgroupTokens) is finished
-// here, by its one workgroup (ONE).
-template <typename T, int L, int V, int N, int BT, bool ONE, bool VEC>
+// First launch.  A batch of one run of at most ONE tokens is finished here, by
+// its one workgroup (ONE = 0: there are more runs).
+template <typename T, int L, int V, int N, int BT, int ONE, bool VEC>
 __global__ __launch_bounds__(BT) void k_route_select(RouteArgs a) {
     __shared__ int32_t hist[L * V + kMaxShared + 1];
     __shared__ __attribute__((aligned(16))) float psum[kSumRows<L, BT> * L * V];
     const int tid = threadIdx.x;
     const int64_t t0 = (int64_t)blockIdx.x * a.CT, t1 = t0 + a.CT < a.T ? t0 + a.CT : a.T;
     route_select<T, L, V, N, BT, VEC>(a, t0, t1, hist, psum);
-    if constexpr (ONE) {
+    if constexpr (ONE > 0) {
         constexpr int H = 4;
         __shared__ int32_t base[L * V + kMaxShared + 1];
-        __shared__ PlaceTable<H, BT, kOneWorkgroupTokens / 32> tab;
+        __shared__ PlaceTable<H, BT, ONE / 32, L * V + kMaxShared> tab;
         Choices<H> c;
         const int step = tab.step(a);
         c.load(a, 0, (int)(a.T < step ? a.T : step) * a.kk);
@@ -626,7 +628,7 @@ __global__ __launch_bounds__(BT) void k_route_select(RouteArgs a) {
         route_counts(a, hist, base);
         const int64_t used = base[a.G];
         __syncthreads();
-        route_place<H, BT>(a, 0, a.T, base, tab, c);
+        route_place(a, 0, a.T, base, tab, c);
         route_tail(a, used, tid, BT);
     } else {
         for (int i = tid; i < a.ldh; i += BT) {
@@ -699,16 +701,16 @@ __device__ __forceinline__ void route_totals(const RouteArgs &a, int b, int32_t 
     __syncthreads();
 }
 
-// Second launch: workgroup b < nwg places the rows of its run; workgroup nwg
-// sums the probabilities.  Every workgroup adds up the histograms of all runs
+// Second launch: workgroup b < nwg places the rows of its run; the last one of
+// the grid sums the probabilities.  Every workgroup adds up the histograms of all runs
 // by itself (what precedes its run, and the totals): about 256 rows of G + 1
 // bytes (or 2-byte words) from L2, which is less than a third launch costs.
-template <typename HT, int NT, int W>
-__global__ __launch_bounds__(NT) void k_route_place(RouteArgs a) {
+template <typename HT, int NT, int W, int GROUPS>
+__global__ __launch_bounds__(NT, 4) void k_route_place(RouteArgs a) {
     constexpr int H = 4;
-    __shared__ int32_t tot[kMaxGroups + 16], before[kMaxGroups + 16], base[kMaxGroups + 1];
-    __shared__ PlaceTable<H, NT, W> tab;
-    __shared__ __attribute__((aligned(16))) float red[4 * NT + 1024];
+    __shared__ int32_t tot[GROUPS + 16], before[GROUPS + 16], base[GROUPS + 1];
+    __shared__ PlaceTable<H, NT, W, GROUPS> tab;
+    __shared__ __attribute__((aligned(16))) float red[4 * NT];
     const int tid = threadIdx.x, b = blockIdx.x;
     const int64_t t0 = (int64_t)b * a.CT, t1 = t0 + a.CT < a.T ? t0 + a.CT : a.T;
     Choices<H> c;
@@ -718,74 +720,80 @@ __global__ __launch_bounds__(NT) void k_route_place(RouteArgs a) {
         tab.clear(a);
     }
     route_totals<HT, NT>(a, b, tot, before);
-    if (b == a.nwg) {                       // the loss's workgroup
-        // red: [parts][lde], at most 4 floats per thread, then the sums
-        const int quads = a.lde / 4, parts = NT / quads, part = tid / quads, q = tid % quads;
-        if (part < parts) {
-            constexpr int U = 4;
-            const float4 *x = reinterpret_cast<const float4 *>(a.part);
-            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int w = part; w < a.nwg; w += U * parts) {
-                float4 v[U];
+    if (b < a.nwg) {
+        exclusive_scan(tot, base, a.G);   // group starts; base[G] is the rows in use
+        __syncthreads();
+        const int64_t used = base[a.G];
+        if (b == 0) {
+            route_counts(a, tot, base);
+            __syncthreads();
+        }
+        for (int i = tid; i < a.G; i += NT) base[i] += before[i];
+        __syncthreads();
+        route_place(a, t0, t1, base, tab, c);
+        route_tail(a, used, (int64_t)b * NT + tid, (int64_t)a.nwg * NT);
+    }
+    if (!a.prob_sum || b != (int)gridDim.x - 1) return;
+    // the loss, by a workgroup of its own or the last run's
+    const int quads = a.lde / 4, parts = NT / quads, part = tid / quads, q = tid % quads;
+    if (part < parts) {
+        constexpr int U = 4;
+        const float4 *x = reinterpret_cast<const float4 *>(a.part);
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = part; w < a.nwg; w += U * parts) {
+            float4 v[U];
 #pragma unroll
-                for (int u = 0; u < U; u++) v[u] = x[(int64_t)(w + u * parts < a.nwg ? w + u * parts : 0) * quads + q];
+            for (int u = 0; u < U; u++) v[u] = x[(int64_t)(w + u * parts < a.nwg ? w + u * parts : 0) * quads + q];
 #pragma unroll
-                for (int u = 0; u < U; u++) {
-                    const bool in = w + u * parts < a.nwg;
-                    s.x += in ? v[u].x : 0.0f;
-                    s.y += in ? v[u].y : 0.0f;
-                    s.z += in ? v[u].z : 0.0f;
-                    s.w += in ? v[u].w : 0.0f;
-                }
+            for (int u = 0; u < U; u++) {
+                const bool in = w + u * parts < a.nwg;
+                s.x += in ? v[u].x : 0.0f;
+                s.y += in ? v[u].y : 0.0f;
+                s.z += in ? v[u].z : 0.0f;
+                s.w += in ? v[u].w : 0.0f;
             }
-            reinterpret_cast<float4 *>(red)[part * quads + q] = s;
         }
-        __syncthreads();
-        float *sum = red + 4 * NT;
-        for (int e = tid; e < a.E; e += NT) {
-            float s = 0.0f;
-            for (int w = 0; w < parts; w++) s += red[w * a.lde + e];
-            sum[e] = s;
-            a.prob_sum[e] = s;
-        }
-        __syncthreads();
-        if (tid < 64) route_loss(a, tot, sum);
-        return;
+        reinterpret_cast<float4 *>(red)[part * quads + q] = s;   // [parts][lde]
     }
-    exclusive_scan(tot, base, a.G);   // group starts; base[G] is the rows in use
     __syncthreads();
-    const int64_t used = base[a.G];
-    if (b == 0) {
-        route_counts(a, tot, base);
-        __syncthreads();
+    float *sum = reinterpret_cast<float *>(before);              // of use to nobody any more
+    for (int e = tid; e < a.E; e += NT) {
+        float s = 0.0f;
+        for (int w = 0; w < parts; w++) s += red[w * a.lde + e];
+        sum[e] = s;
+        a.prob_sum[e] = s;
     }
-    for (int i = tid; i < a.G; i += NT) base[i] += before[i];
     __syncthreads();
-    route_place<H, NT, W>(a, t0, t1, base, tab, c);
-    route_tail(a, used, (int64_t)b * NT + tid, (int64_t)a.nwg * NT);
+    if (tid < 64) route_loss(a, tot, sum);
 }
 
 static int32_t round_up(int64_t n, int64_t m) { return (int32_t)((n + m - 1) / m * m); }
 
 // Runs of whole words of tokens, about one to a compute unit (the placing reads
 // every run's histogram in every workgroup), with counts below 2^16.
-static void route_runs(int64_t T, int32_t &CT, int32_t &nwg) {
-    CT = T <= kOneWorkgroupTokens ? (int32_t)kOneWorkgroupTokens
-                                  : T >= 256 * 65504ll ? 65504 : round_up((T + 255) / 256, 32);
+static void route_runs(int64_t T, int64_t E, int64_t k, int32_t &CT, int32_t &nwg) {
+    const int64_t one = k <= 8 && E <= 256 ? kOneLargeTokens : kOneSmallTokens;
+    CT = T <= one ? (int32_t)one : T >= 256 * 65504ll ? 65504 : round_up((T + 255) / 256, 32);
     nwg = (int32_t)((T + CT - 1) / CT);
 }
 
-int64_t route_workspace_bytes(int64_t T, int64_t E, int64_t shared) {
+int64_t route_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t shared) {
     int32_t CT, nwg;
-    route_runs(T, CT, nwg);
+    route_runs(T, E, k, CT, nwg);
     return nwg == 1 ? 0 : (int64_t)nwg * ((CT > 255 ? 2 : 1) * round_up(E + shared + 1, 16) + 4 * round_up(E, 4));
 }
 
 template <typename T, int L, int V, int N, bool VEC>
 static void route_launch_few(const RouteArgs &a, hipStream_t s) {
     constexpr int B = N == 8 && L > 8 && L * V <= 512 ? 512 : 256;
-    if (a.nwg == 1) k_route_select<T, L, V, N, 256, true, VEC><<<1, 256, 0, s>>>(a);
-    else k_route_select<T, L, V, N, B, false, VEC><<<a.nwg, B, 0, s>>>(a);
+    if (a.T <= kOneSmallTokens) {
+        k_route_select<T, L, V, N, 256, kOneSmallTokens, VEC><<<1, 256, 0, s>>>(a);
+    } else if (a.nwg > 1) {
+        k_route_select<T, L, V, N, B, 0, VEC><<<a.nwg, B, 0, s>>>(a);
+    } else {
+        constexpr int B1 = VEC ? 1024 : 512;   // what the registers allow
+        if constexpr (N == 8 && L * V <= 256) k_route_select<T, L, V, N, B1, kOneLargeTokens, VEC><<<1, B1, 0, s>>>(a);
+    }
 }
 template <typename T, int L, int V, bool VEC>
 static void route_few(const RouteArgs &a, hipStream_t s) {
@@ -808,20 +816,27 @@ template <typename T>
 static void route_dispatch(const RouteArgs &a, bool vec, hipStream_t s) {
     if (a.T >= kManyTokens && a.k <= 8 && a.E <= 256 && vec) {
         constexpr int B = kManyThreads;
-        if (a.E <= 64) k_route_select<T, 4, 16, 8, B, false, true><<<a.nwg, B, 0, s>>>(a);
-        else if (a.E <= 128) k_route_select<T, 4, 32, 8, B, false, true><<<a.nwg, B, 0, s>>>(a);
-        else k_route_select<T, 8, 32, 8, B, false, true><<<a.nwg, B, 0, s>>>(a);
+        if (a.E <= 64) k_route_select<T, 4, 16, 8, B, 0, true><<<a.nwg, B, 0, s>>>(a);
+        else if (a.E <= 128) k_route_select<T, 4, 32, 8, B, 0, true><<<a.nwg, B, 0, s>>>(a);
+        else k_route_select<T, 8, 32, 8, B, 0, true><<<a.nwg, B, 0, s>>>(a);
     } else if (vec) {
         route_few_experts<T, true>(a, s);
     } else {
         route_few_experts<T, false>(a, s);
     }
     if (a.nwg == 1) return;
-    const unsigned grid = (unsigned)(a.nwg + (a.prob_sum ? 1 : 0));
-    if (a.CT > 255 && a.G <= kManyWordsGroups) k_route_place<uint16_t, 1024, 16><<<grid, 1024, 0, s>>>(a);
-    else if (a.CT > 255) k_route_place<uint16_t, 1024, 8><<<grid, 1024, 0, s>>>(a);
-    else if (a.CT > 32) k_route_place<uint8_t, 512, 8><<<grid, 512, 0, s>>>(a);
-    else k_route_place<uint8_t, 512, 1><<<grid, 512, 0, s>>>(a);
+    // The loss has a workgroup of its own, except beside 1024-thread workgroups,
+    // of which a compute unit holds one: 257 of them would be two rounds.
+    const unsigned grid = (unsigned)(a.nwg + (a.prob_sum && a.CT <= 255 ? 1 : 0));
+    if (a.CT > 255) {
+        if (a.G <= kFewGroups) k_route_place<uint16_t, 1024, 16, kFewGroups><<<a.nwg, 1024, 0, s>>>(a);
+        else k_route_place<uint16_t, 1024, 8, kMaxGroups><<<a.nwg, 1024, 0, s>>>(a);
+    } else if (a.CT > 32) {
+        if (a.G <= kFewGroups) k_route_place<uint8_t, 512, 8, kFewGroups><<<grid, 512, 0, s>>>(a);
+        else k_route_place<uint8_t, 512, 8, kMaxGroups><<<grid, 512, 0, s>>>(a);
+    } else {
+        k_route_place<uint8_t, 512, 1, kMaxGroups><<<grid, 512, 0, s>>>(a);
+    }
 }
 
 // Whole 16-byte pieces: pointers are 16-byte aligned (checked at the C ABI).
@@ -841,7 +856,7 @@ hipError_t launch_route(const void *logits, int dtype, int64_t T, int64_t E, int
     const bool vec = whole_pieces(E, ldl, dtype);
     a.experts = experts; a.counts = counts; a.src = src; a.pos = pos;
     a.weights = weights; a.row_weights = row_weights; a.prob_sum = prob_sum; a.loss = loss; a.off = off;
-    route_runs(T, a.CT, a.nwg);
+    route_runs(T, E, k, a.CT, a.nwg);
     a.ldh = round_up(E + shared + 1, 16);
     a.lde = round_up(E, 4);
     a.hist = workspace;

@@ -94,7 +94,7 @@ def _declare(lib):
     lib.bsp_gemm_workspace_size.argtypes = [INT, INT, I64, I64, I64, I64]
     lib.bsp_gemm_workspace_size.restype = SZ
     lib.bsp_moe_route.argtypes = [P, INT, I64, I64, I64, P, I64, I64, P, P, P, P, P, P, P, P, P, U32, P, SZ, P]
-    lib.bsp_moe_route_workspace_size.argtypes = [I64, I64, I64]
+    lib.bsp_moe_route_workspace_size.argtypes = [I64, I64, I64, I64]
     lib.bsp_moe_route_workspace_size.restype = SZ
     lib.bsp_moe_route_backward.argtypes = [P, INT, I64, I64, I64, P, I64, I64, P, P, P, P, P, P, I64, U32, P]
     lib.bsp_swiglu_checkpoint.argtypes = [P, INT, I64, I64, P, P, P, P, P, P, P, P]
@@ -679,8 +679,8 @@ def _ld(t):
     return ld if ld >= cols or t.shape[0] > 1 else cols
 
 
-def moe_route_workspace_size(T: int, E: int, shared: int = 0) -> int:
-    return int(_lib_raw().bsp_moe_route_workspace_size(T, E, shared))
+def moe_route_workspace_size(T: int, E: int, k: int, shared: int = 0) -> int:
+    return int(_lib_raw().bsp_moe_route_workspace_size(T, E, k, shared))
 
 
 def moe_route(logits: torch.Tensor, k: int, norm: bool = True, shared: int = 0, token_mask=None, aux: bool = False,
@@ -721,7 +721,7 @@ def moe_route(logits: torch.Tensor, k: int, norm: bool = True, shared: int = 0, 
             _dev_ptr(get("prob_sum"), "prob_sum", dev, "f32", E) if aux else None,
             _dev_ptr(get("loss"), "loss", dev, "f32", 1) if aux else None)
     lib = _lib_raw()
-    need = lib.bsp_moe_route_workspace_size(T, E, shared)
+    need = lib.bsp_moe_route_workspace_size(T, E, k, shared)
     if workspace is None and need:
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     ws = _opt_ptr(workspace, "workspace", dev, "u8", need)

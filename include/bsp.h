@@ -134,7 +134,8 @@ bsp_status bsp_quantize_nvfp4_per_token(const uint16_t *x, int64_t M, int64_t K,
  *                Grouped: ld_colT >= roundup32(M + 31 G) (the value of
  *                bsp_mxfp8_grouped_cols(M, G) keeps rows line-aligned).
  *   group_offsets  device int64 [G+1] or NULL.  Rows [off[g], off[g+1]) form
- *                group g (0 = off[0] <= ... <= off[G] = M).  Columnwise blocks
+ *                group g (0 = off[0] <= ... <= off[G] <= M; rows from off[G]
+ *                on have no group and are left out).  Columnwise blocks
  *                then stay inside a group: group g occupies transposed columns
  *                [P[g], P[g] + pad32(n_g)) with P the running sum of the padded
  *                sizes; padding columns hold code 0.  Columns from P[G] to
@@ -471,7 +472,7 @@ bsp_status bsp_swiglu_quantize(const void *h13, int in_dtype, int64_t R, int64_t
  *   loss     device f32 [1] or NULL (out; both or neither):
  *            E / (k n^2) sum_{e < E} counts_e Q_e (1 when both are uniform; 0
  *            for n = 0)
- *   workspace  device, >= bsp_moe_route_workspace_size(T, E, shared) bytes
+ *   workspace  device, >= bsp_moe_route_workspace_size(T, E, k, shared) bytes
  * group_offsets and src are the grouped GEMMs' and quantizers' row map with
  * M = T kk; with padding tokens group_offsets[G] < M, and those calls leave
  * the rows of C past it untouched.  Sums are f32 in a fixed order: results
@@ -583,7 +584,7 @@ size_t bsp_gemm_workspace_size(int fmt, int mode, int64_t M, int64_t N, int64_t 
 size_t bsp_gemm_bf16_workspace_size(int mode, int64_t M, int64_t N, int64_t K, int64_t G);
 /* Bytes of workspace for bsp_moe_route (0 for invalid arguments, and for
  * batches small enough to need none). */
-size_t bsp_moe_route_workspace_size(int64_t T, int64_t E, int64_t shared);
+size_t bsp_moe_route_workspace_size(int64_t T, int64_t E, int64_t k, int64_t shared);
 
 #ifdef __cplusplus
 }

@@ -69,6 +69,11 @@ CASES = [
     (64, 128, 8, 1, "bf16", True, "ties", 0.3, 8),
     (65, 129, 17, 64, "f32", False, "unavailable", 0.1, 1),
     (100, 65, 16, 0, "bf16", True, "wide", 0.0, 0),
+    (130, 128, 8, 0, "f32", True, "ties", 0.0, 0),
+    (256, 200, 7, 5, "bf16", False, "unavailable", 0.2, 0),
+    (255, 64, 8, 0, "f32", True, "lowest", 0.0, 1),
+    (257, 256, 8, 1, "f32", True, "normal", 0.0, 0),
+    (256, 257, 8, 1, "f32", True, "normal", 0.0, 0),
     (300, 256, 8, 1, "bf16", True, "unavailable", 0.1, 0),
     (1000, 128, 8, 0, "f32", True, "normal", 0.0, 0),
     (1025, 96, 6, 0, "f32", False, "lowest", 0.0, 4),
@@ -181,7 +186,7 @@ def test_results_repeat_bit_for_bit_and_buffers_are_reused():
     xd, _ = logits_of(10, 3000, 128, torch.float32)
     a = ops.moe_route(xd, 8, aux=True)
     saved = {k: v.clone() for k, v in a.items()}
-    ws = torch.full((ops.moe_route_workspace_size(3000, 128),), 0xAB, dtype=torch.uint8, device=DEV)
+    ws = torch.full((ops.moe_route_workspace_size(3000, 128, 8),), 0xAB, dtype=torch.uint8, device=DEV)
     for t in a.values():
         t.fill_(77)
     b = ops.moe_route(xd, 8, aux=True, out=a, workspace=ws)
@@ -204,7 +209,7 @@ def test_route_on_another_stream_and_in_a_graph():
     grad = ops.moe_route_backward(xd, 6, eager["experts"], eager["counts"], eager["pos"], d_weights=d, d_loss=one)
     out = {k: torch.empty_like(v) for k, v in eager.items()}
     gout = torch.empty_like(grad)
-    ws = torch.empty(ops.moe_route_workspace_size(900, 96), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(ops.moe_route_workspace_size(900, 96, 6), dtype=torch.uint8, device=DEV)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         ops.moe_route(xd, 6, aux=True, out=out, workspace=ws)
@@ -278,3 +283,23 @@ def test_row_map_drives_the_grouped_gemm_with_padding_tokens():
     got = host(out)
     assert np.all(np.abs(got[:used] - want) <= 1e-3 * size)
     assert np.all(got[used:] == 5.0)
+
+
+def test_row_map_drives_the_grouped_quantizer_with_padding_tokens():
+    """The columnwise copy of grouped rows stops at group_offsets[G], as if the rows past it were not there."""
+    T, E, k, H = 150, 5, 3, 64
+    xd, _ = logits_of(13, T, E, torch.float32)
+    mask = np.random.default_rng(2).random(T) >= 0.4
+    r = ops.moe_route(xd, k, token_mask=to_dev(mask))
+    off = r["group_offsets"]
+    used = int(off[-1])
+    assert 0 < used < T * k
+    x = torch.randn(T, H, device=DEV).to(torch.bfloat16)
+    ld = ops.mxfp8_grouped_cols(T * k, E)
+
+    def copy(gather):
+        out = {"codes_colT": torch.full((H, ld), 0x5A, dtype=torch.uint8, device=DEV),
+               "scales_colT": torch.full((H, ld // 32), 0x5A, dtype=torch.uint8, device=DEV)}
+        return ops.quantize_mxfp8(x, False, True, group_offsets=off, row_gather=gather, out=out)
+    a, b = copy(r["src"]), copy(r["src"][:used].contiguous())
+    assert torch.equal(a["codes_colT"], b["codes_colT"]) and torch.equal(a["scales_colT"], b["scales_colT"])

@@ -38,16 +38,17 @@ def test_route_refusals():
     assert route(E=4, ld=4, k=5) == SHAPE
     assert route(shared=-1) == SHAPE and route(shared=65) == SHAPE
     assert route(T=1 << 29) == SHAPE                                    # T * kk past 31 bits
-    assert route(ws=None) == WORKSPACE and route(nb=L.bsp_moe_route_workspace_size(500, 64, 0) - 1) == WORKSPACE
+    assert route(ws=None) == WORKSPACE and route(nb=L.bsp_moe_route_workspace_size(500, 64, 4, 0) - 1) == WORKSPACE
     assert route(logits=MIS) == ALIGN and route(mask=MIS) == ALIGN and route(ps=MIS, loss=A) == ALIGN
 
 
 def test_route_workspace_size():
     ws = L.bsp_moe_route_workspace_size
-    assert ws(0, 64, 0) == 0 and ws(100, 0, 0) == 0 and ws(100, 2000, 0) == 0 and ws(100, 64, -1) == 0
-    assert ws(1, 64, 0) == 0                                            # one workgroup, nothing to exchange
-    assert 0 < ws(1000, 64, 0) < ws(1000, 128, 1) < ws(8192, 128, 1)
-    assert ws(1 << 24, 1024, 64) < 16 << 20                             # bounded by the number of runs
+    assert ws(0, 64, 4, 0) == 0 and ws(1000, 0, 4, 0) == 0 and ws(1000, 2000, 4, 0) == 0 and ws(1000, 64, 4, -1) == 0
+    assert ws(1000, 64, 0, 0) == 0 and ws(1000, 64, 65, 0) == 0
+    assert ws(1, 64, 4, 0) == 0                                         # one workgroup, nothing to exchange
+    assert 0 < ws(1000, 64, 4, 0) < ws(1000, 128, 4, 1) < ws(8192, 128, 4, 1)
+    assert ws(1 << 24, 1024, 4, 64) < 16 << 20                          # bounded by the number of runs
 
 
 def test_route_backward_refusals():
