@@ -645,8 +645,8 @@ def swiglu_quantize(h13: torch.Tensor, fmt: int = -1, mode46: bool = False, retu
 def _dev_ptr(t, name, dev, kind, numel):
     """_arg for a required contiguous tensor of one dtype, in one expression when all is well (a call for a single
     token is bound by such checks); returns the pointer."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is _DT[kind] and t.device == dev and t.is_contiguous()
-            and t.numel() >= numel):
+    if not (isinstance(t, torch.Tensor) and t.dtype is _DT[kind] and t.is_contiguous() and t.numel() >= numel
+            and t.device == dev):
         _arg(t, name, dev, kind, numel)
     return t.data_ptr()
 
@@ -703,15 +703,15 @@ def moe_route(logits: torch.Tensor, k: int, norm: bool = True, shared: int = 0, 
     R = T * kk
     if out is None:
         i32, f32 = torch.int32, torch.float32
-        out = {"experts": torch.empty((T, kk), dtype=i32, device=dev),
-               "weights": torch.empty((T, kk), dtype=f32, device=dev),
-               "counts": torch.empty((G + 1,), dtype=i32, device=dev),
-               "group_offsets": torch.empty((G + 1,), dtype=torch.int64, device=dev),
-               "src": torch.empty((R,), dtype=i32, device=dev), "pos": torch.empty((T, kk), dtype=i32, device=dev),
-               "row_weights": torch.empty((R,), dtype=f32, device=dev)}
+        out = {"experts": torch.empty(T, kk, dtype=i32, device=dev),
+               "weights": torch.empty(T, kk, dtype=f32, device=dev),
+               "counts": torch.empty(G + 1, dtype=i32, device=dev),
+               "group_offsets": torch.empty(G + 1, dtype=torch.int64, device=dev),
+               "src": torch.empty(R, dtype=i32, device=dev), "pos": torch.empty(T, kk, dtype=i32, device=dev),
+               "row_weights": torch.empty(R, dtype=f32, device=dev)}
         if aux:
-            out["prob_sum"] = torch.empty((E,), dtype=f32, device=dev)
-            out["loss"] = torch.empty((1,), dtype=f32, device=dev)
+            out["prob_sum"] = torch.empty(E, dtype=f32, device=dev)
+            out["loss"] = torch.empty(1, dtype=f32, device=dev)
     get = out.get
     ptrs = (_dev_ptr(get("experts"), "experts", dev, "i32", R), _dev_ptr(get("weights"), "weights", dev, "f32", R),
             _dev_ptr(get("counts"), "counts", dev, "i32", G + 1),
@@ -723,7 +723,7 @@ def moe_route(logits: torch.Tensor, k: int, norm: bool = True, shared: int = 0, 
     lib = _lib_raw()
     need = lib.bsp_moe_route_workspace_size(T, E, k, shared)
     if workspace is None and need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws = _opt_ptr(workspace, "workspace", dev, "u8", need)
     st = lib.bsp_moe_route(logits.data_ptr(), dt, T, E, _ld(logits), mask, k, shared, *ptrs, ROUTE_NORM if norm else 0,
                            ws, need, _stream(dev))
@@ -747,7 +747,7 @@ def moe_route_backward(logits: torch.Tensor, k: int, experts, counts, pos, d_wei
             _dev_ptr(counts, "counts", dev, "i32", E + shared + 1),
             _opt_ptr(d_weights, "d_weights", dev, "f32", T * kk), _opt_ptr(d_loss, "d_loss", dev, "f32", 1))
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        out = torch.empty(T, E, dtype=logits.dtype, device=dev)
     else:
         _matrix_arg(out, "out", dev, logits.dtype)
         if out.shape != logits.shape:
@@ -756,6 +756,17 @@ def moe_route_backward(logits: torch.Tensor, k: int, experts, counts, pos, d_wei
                                            out.data_ptr(), _ld(out), ROUTE_NORM if norm else 0, _stream(dev))
     _check(st, "bsp_moe_route_backward")
     return out
+
+
+def _values_arg(t, name):
+    """A contiguous 2-D f32 or bf16 tensor; returns (rows, columns, device, C dtype)."""
+    if not (isinstance(t, torch.Tensor) and t.is_contiguous() and t.device.type == DEVICE_TYPE
+            and (t.dtype is torch.bfloat16 or t.dtype is torch.float32)):
+        _arg(t, name, t.device if isinstance(t, torch.Tensor) else None, ("f32", "bf16"))
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    return rows, cols, t.device, DTYPE_BF16 if t.dtype is torch.bfloat16 else DTYPE_F32
 
 
 def swiglu_checkpoint(h13: torch.Tensor, row_weights=None, n_rows=None, return_h: bool = True,
@@ -767,31 +778,26 @@ def swiglu_checkpoint(h13: torch.Tensor, row_weights=None, n_rows=None, return_h
     n_rows: device i64 scalar, the rows in use (e.g. group_offsets[G:]); outputs of the others are zeros.
     See bsp_swiglu_checkpoint in include/bsp.h.
     """
-    _arg(h13, "h13", h13.device if isinstance(h13, torch.Tensor) else None, ("f32", "bf16"))
-    if h13.dim() != 2:
-        raise ValueError("h13 must be 2-D [R, 2I]")
-    R, I2 = h13.shape
+    R, I2, dev, dt = _values_arg(h13, "h13")
     if I2 % 64:
         raise ValueError(f"h13 has {I2} columns, needs a multiple of 64")
     I = I2 // 2
-    dev = h13.device
     rw = _opt_ptr(row_weights, "row_weights", dev, "f32", R)
     nr = _opt_ptr(n_rows, "n_rows", dev, "i64", 1)
     if out is None:
-        out = {"ckpt_codes": torch.empty((R, I2), dtype=torch.uint8, device=dev),
-               "ckpt_scales": torch.empty((R, I2 // 32), dtype=torch.uint8, device=dev)}
+        out = {"ckpt_codes": torch.empty(R, I2, dtype=torch.uint8, device=dev),
+               "ckpt_scales": torch.empty(R, I2 // 32, dtype=torch.uint8, device=dev)}
         if return_h:
-            out["h"] = torch.empty((R, I), dtype=torch.bfloat16, device=dev)
+            out["h"] = torch.empty(R, I, dtype=torch.bfloat16, device=dev)
         if quantize_h:
-            out["codes"] = torch.empty((R, I), dtype=torch.uint8, device=dev)
-            out["scales"] = torch.empty((R, I // 32), dtype=torch.uint8, device=dev)
+            out["codes"] = torch.empty(R, I, dtype=torch.uint8, device=dev)
+            out["scales"] = torch.empty(R, I // 32, dtype=torch.uint8, device=dev)
     get = out.get
     ptrs = (_dev_ptr(get("h"), "h", dev, "bf16", R * I) if return_h else None,
             _dev_ptr(get("codes"), "codes", dev, "u8", R * I) if quantize_h else None,
             _dev_ptr(get("scales"), "scales", dev, "u8", R * (I // 32)) if quantize_h else None,
             _dev_ptr(get("ckpt_codes"), "ckpt_codes", dev, "u8", R * I2),
             _dev_ptr(get("ckpt_scales"), "ckpt_scales", dev, "u8", R * (I2 // 32)))
-    dt = DTYPE_BF16 if h13.dtype == torch.bfloat16 else DTYPE_F32
     st = _lib_raw().bsp_swiglu_checkpoint(h13.data_ptr(), dt, R, I, rw, nr, *ptrs, _stream(dev))
     _check(st, "bsp_swiglu_checkpoint")
     return out
@@ -802,29 +808,26 @@ def swiglu_checkpoint_backward(dh: torch.Tensor, ckpt_codes, ckpt_scales, row_we
     """dh [R, I] (f32 or bf16) and the checkpoint -> dict: 'dh13' [R, 2I] in dh's dtype, 'h' bf16 [R, I] computed
     again (unless return_h is False) and, with row_weights, 'd_row_weights' f32 [R].
     See bsp_swiglu_checkpoint_backward in include/bsp.h."""
-    _arg(dh, "dh", dh.device if isinstance(dh, torch.Tensor) else None, ("f32", "bf16"))
-    if dh.dim() != 2 or dh.shape[1] % 32:
-        raise ValueError("dh must be 2-D [R, I] with I a multiple of 32")
-    R, I = dh.shape
-    dev = dh.device
+    R, I, dev, dt = _values_arg(dh, "dh")
+    if I % 32:
+        raise ValueError(f"dh has {I} columns, needs a multiple of 32")
     cc = _dev_ptr(ckpt_codes, "ckpt_codes", dev, "u8", R * 2 * I)
     cs = _dev_ptr(ckpt_scales, "ckpt_scales", dev, "u8", R * (2 * I // 32))
     rw = _opt_ptr(row_weights, "row_weights", dev, "f32", R)
     nr = _opt_ptr(n_rows, "n_rows", dev, "i64", 1)
     weighted = row_weights is not None
     if out is None:
-        out = {"dh13": torch.empty((R, 2 * I), dtype=dh.dtype, device=dev)}
+        out = {"dh13": torch.empty(R, 2 * I, dtype=dh.dtype, device=dev)}
         if return_h:
-            out["h"] = torch.empty((R, I), dtype=torch.bfloat16, device=dev)
+            out["h"] = torch.empty(R, I, dtype=torch.bfloat16, device=dev)
         if weighted:
-            out["d_row_weights"] = torch.empty((R,), dtype=torch.float32, device=dev)
-    bf = dh.dtype == torch.bfloat16
+            out["d_row_weights"] = torch.empty(R, dtype=torch.float32, device=dev)
     get = out.get
-    ptrs = (_dev_ptr(get("dh13"), "dh13", dev, "bf16" if bf else "f32", R * 2 * I),
+    ptrs = (_dev_ptr(get("dh13"), "dh13", dev, "bf16" if dt == DTYPE_BF16 else "f32", R * 2 * I),
             _dev_ptr(get("h"), "h", dev, "bf16", R * I) if return_h else None,
             _dev_ptr(get("d_row_weights"), "d_row_weights", dev, "f32", R) if weighted else None)
-    st = _lib_raw().bsp_swiglu_checkpoint_backward(dh.data_ptr(), DTYPE_BF16 if bf else DTYPE_F32, R, I, cc, cs, rw,
-                                                   nr, *ptrs, _stream(dev))
+    st = _lib_raw().bsp_swiglu_checkpoint_backward(dh.data_ptr(), dt, R, I, cc, cs, rw, nr,
+                                                   *ptrs, _stream(dev))
     _check(st, "bsp_swiglu_checkpoint_backward")
     return out
 
@@ -842,7 +845,7 @@ def moe_combine(y: torch.Tensor, pos, weights=None, out_dtype=None, out=None):
     pp = _dev_ptr(pos, "pos", dev, "i32", T * kk)
     wp = _opt_ptr(weights, "weights", dev, "f32", T * kk)
     if out is None:
-        out = torch.empty((T, H), dtype=out_dtype or y.dtype, device=dev)
+        out = torch.empty(T, H, dtype=out_dtype or y.dtype, device=dev)
     do = _matrix_arg(out, "out", dev)
     if out.shape != (T, H):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, H)}")
