@@ -472,11 +472,14 @@ struct Choices {
             if (h * nt < n) {
                 const int i = h * nt + tid;
                 const int64_t c = s0 * a.kk + (i < n ? i : 0);
-                const int e = a.experts[c];
+                g[h] = a.experts[c];   // not looked at here: that would wait for it
                 w[h] = a.weights[c];
-                g[h] = i < n ? e : -1;
             }
         }
+    }
+    // group of choice h of a pass of n, -1 for none
+    __device__ __forceinline__ int group(int h, int n) const {
+        return h * (int)blockDim.x + (int)threadIdx.x < n ? g[h] : -1;
     }
 };
 template <int H, int NT, int W, int GROUPS>
@@ -513,7 +516,8 @@ __device__ __forceinline__ void route_place(const RouteArgs &a, int64_t t0, int6
 #pragma unroll
             for (int h = 0; h < H; h++) {
                 tok[h] = t;
-                if (c.g[h] >= 0) atomicOr(&tab.bits[c.g[h] * W + (t >> 5)], 1u << (t & 31));
+                const int g = c.group(h, n);
+                if (g >= 0) atomicOr(&tab.bits[g * W + (t >> 5)], 1u << (t & 31));
                 t += dq + (r + dr >= a.kk ? 1 : 0);
                 r += dr - (r + dr >= a.kk ? a.kk : 0);
             }
@@ -544,7 +548,7 @@ __device__ __forceinline__ void route_place(const RouteArgs &a, int64_t t0, int6
         }
 #pragma unroll
         for (int h = 0; h < H; h++) {
-            const int i = h * NT + tid, g = c.g[h], t = tok[h];
+            const int i = h * NT + tid, g = c.group(h, n), t = tok[h];
             int32_t p = -1;
             if (g >= 0) {
                 const uint32_t *b = tab.bits + g * W;
