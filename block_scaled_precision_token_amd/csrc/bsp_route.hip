@@ -14,6 +14,9 @@
 namespace bsp {
 
 constexpr float kLog2e = 1.44269504088896341f;
+// From here on fewer lanes to a token pay: choice of 16384 f32 tokens 5.6 us
+// instead of 6.7 for 64 experts and 9.4 instead of 10.2 for 256 (the same for
+// 128), 24000 tokens 6.2 / 8.6 and 10.1 / 12.2; below, 4096 x 128 6.4 instead of 5.1.
 constexpr int64_t kManyTokens = 16384;
 constexpr int64_t kBwdWorkgroups = 768;   // three to a compute unit, as the registers of the widest form allow
 // Batches that one workgroup finishes in one launch: of 256 threads, or of 1024
@@ -23,6 +26,7 @@ constexpr int64_t kOneSmallTokens = 64, kOneLargeTokens = 128;
 constexpr int kMaxShared = 64;
 constexpr int kMaxGroups = 1024 + kMaxShared;
 constexpr int kFewGroups = kMaxGroups / 2;   // placing: groups of the smaller rank table
+constexpr int kSums = 8, kMaxSlice = 1024 / 4 / kSums;   // workgroups that sum the probabilities, their quads of experts
 
 // Lane exchanges within a row of 16 by DPP.  A token's L lanes (4, 8, 16 or 32)
 // reduce over mirror(16), mirror(8), xor 2, xor 1, each step joining two
@@ -273,9 +277,10 @@ struct RouteArgs {
     int64_t *off;
     // workspace, one entry per workgroup (a run of CT consecutive tokens)
     int32_t CT, nwg, ldh, lde;
-    void *hist;       // rows of each group, then routed tokens, zeros up to ldh; u8 or (CT > 255) u16,
-                      // in 16-byte pieces of columns: [piece][nwg][16 bytes]
+    void *hist;       // rows of each group, then routed tokens: [G + 1][ldh], u8 or (CT > 255) u16 to a run
     float *part;      // [nwg][lde]: sums of probabilities, zeros
+    int32_t slice;    // quads of experts whose sums over the runs one workgroup takes: 1, 2, .. 32
+    uint64_t *loss_sum;   // see route_sums
 };
 
 // Choice, weights, histogram and probability sums of tokens [t0, t1) by one
@@ -392,21 +397,18 @@ __device__ __forceinline__ void route_select(const RouteArgs &a, int64_t t0, int
     __syncthreads();
 }
 
+// Expert e's part of the loss but for the factor E / k: (c_e / n) (Q_e / n).
+// n = 0: nothing was routed; 0, or NaN if that was for bad rows.
+__device__ __forceinline__ float loss_term(int32_t c, float q, int32_t n) {
+    return n == 0 ? q : ((float)c / (float)n) * (q / (float)n);
+}
 // Loss from the batch's counts and probability sums (LDS), by one wavefront.
 __device__ void route_loss(const RouteArgs &a, const int32_t *tot, const float *q) {
     const int lane = threadIdx.x & 63;
     float s = 0.0f;
-    const float n = (float)tot[a.G];
-    for (int e = lane; e < a.E; e += 64) s += ((float)tot[e] / n) * (q[e] / n);
+    for (int e = lane; e < a.E; e += 64) s += loss_term(tot[e], q[e], tot[a.G]);
     s = wave_sum(s);
-    // n = 0: nothing was routed; 0, or NaN if that was for bad rows
-    if (lane == 0) {
-        float bad = 0.0f;
-        if (tot[a.G] == 0) {
-            for (int e = 0; e < a.E; e++) bad += q[e];
-        }
-        *a.loss = tot[a.G] == 0 ? bad : s * ((float)a.E / (float)a.k);
-    }
+    if (lane == 0) *a.loss = s * ((float)a.E / (float)a.k);
 }
 
 // Inclusive sum over the lanes up to this one, by DPP: within rows of 16, then
@@ -421,29 +423,33 @@ __device__ __forceinline__ int32_t wave_scan(int32_t v) {
     return v;
 }
 
-// Sum over a row of 16 lanes, on all of them.
-__device__ __forceinline__ uint32_t row_sum(uint32_t v) {
-    v += (uint32_t)__builtin_amdgcn_mov_dpp((int)v, DPP_MIRROR16, 0xF, 0xF, true);
-    v += (uint32_t)__builtin_amdgcn_mov_dpp((int)v, DPP_MIRROR8, 0xF, 0xF, true);
-    v += (uint32_t)__builtin_amdgcn_mov_dpp((int)v, DPP_XOR2, 0xF, 0xF, true);
-    v += (uint32_t)__builtin_amdgcn_mov_dpp((int)v, DPP_XOR1, 0xF, 0xF, true);
-    return v;
-}
-
-// Exclusive scan of in[0, n) into out[0, n] (LDS, may be the same), the total
-// last, by the first wavefront; the caller synchronizes.
-__device__ __forceinline__ void exclusive_scan(const int32_t *in, int32_t *out, int n) {
-    if (threadIdx.x >= 64) return;
-    const int per = n / 64 + 1, i0 = threadIdx.x * per, i1 = i0 + per < n ? i0 + per : n;
-    int32_t sum = 0;
-    for (int i = i0; i < i1; i++) sum += in[i];
-    int32_t run = wave_scan(sum) - sum;
-    for (int i = i0; i < i1; i++) {
-        const int32_t v = in[i];
-        out[i] = run;
-        run += v;
+// Exclusive scan of in[0, n) (LDS, n <= kMaxGroups) by a workgroup of NT threads:
+// f(i, sum of the entries before i) for every i; returns the total.  f may
+// store to in.  One wavefront alone, with up to 17 entries to a lane, took 1400
+// cycles for 256 entries, 2300 for 512 and 4900 for 1000; this takes 1100 to 1400.
+template <int NT, typename F>
+__device__ __forceinline__ int32_t exclusive_scan(const int32_t *in, int n, F f) {
+    constexpr int PER = (kMaxGroups + NT - 1) / NT, WAVES = NT / 64;
+    __shared__ int32_t wave_total[WAVES];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int per = (n + NT - 1) / NT, i0 = threadIdx.x * per;
+    int32_t v[PER], sum = 0;
+#pragma unroll
+    for (int q = 0; q < PER; q++) {
+        v[q] = q < per && i0 + q < n ? in[i0 + q] : 0;
+        sum += v[q];
     }
-    if (threadIdx.x == 63) out[n] = run;
+    const int32_t incl = wave_scan(sum);
+    if (lane == 63) wave_total[wave] = incl;
+    __syncthreads();
+    const int32_t upto = wave_scan(lane < WAVES ? wave_total[lane] : 0);
+    int32_t run = incl - sum + (wave > 0 ? __builtin_amdgcn_readlane(upto, wave - 1) : 0);
+#pragma unroll
+    for (int q = 0; q < PER; q++) {
+        if (q < per && i0 + q < n) f(i0 + q, run);
+        run += v[q];
+    }
+    return __builtin_amdgcn_readlane(upto, WAVES - 1);
 }
 
 // Rows of tokens [t0, t1): base[g] is the first row of group g's choices in
@@ -454,23 +460,23 @@ __device__ __forceinline__ void exclusive_scan(const int32_t *in, int32_t *out, 
 // the caller's other work.
 //
 // Longer runs (W >= 8) keep the ranks of the words' first bits beside the
-// table (adding up to 16 words for every choice was half of the kernel), and
+// table (adding up to 16 words for every choice took longer than the rest), and
 // put the rows in order in LDS to write them group by group: a scattered
 // 4-byte store is an L2 request of its own, and at 600018 choices those of src
 // and row_weights took 3 of 13.5 us; in runs of several rows to a group
 // neighbouring lanes share requests.
-template <int H>
+template <int H, int NT>
 struct Choices {
     int g[H];
     float w[H];
     __device__ __forceinline__ void load(const RouteArgs &a, int64_t s0, int n) {
-        const int tid = threadIdx.x, nt = blockDim.x;
+        const int tid = threadIdx.x;
 #pragma unroll
         for (int h = 0; h < H; h++) {
             g[h] = -1;
             w[h] = 0.0f;
-            if (h * nt < n) {
-                const int i = h * nt + tid;
+            if (h * NT < n) {
+                const int i = h * NT + tid;
                 const int64_t c = s0 * a.kk + (i < n ? i : 0);
                 g[h] = a.experts[c];   // not looked at here: that would wait for it
                 w[h] = a.weights[c];
@@ -479,15 +485,19 @@ struct Choices {
     }
     // group of choice h of a pass of n, -1 for none
     __device__ __forceinline__ int group(int h, int n) const {
-        return h * (int)blockDim.x + (int)threadIdx.x < n ? g[h] : -1;
+        return h * NT + (int)threadIdx.x < n ? g[h] : -1;
     }
 };
 template <int H, int NT, int W, int GROUPS>
 struct PlaceTable {
     static constexpr bool LONG = W >= 8;
-    // 16-byte aligned rows of W words
-    __attribute__((aligned(16))) uint32_t bits[GROUPS * W];
-    __attribute__((aligned(16))) uint16_t rank[LONG ? GROUPS * W : 8];   // of a word's first bit
+    // Strides: rows of 16 bytes' alignment that start at 16 different banks, an
+    // odd multiple of four words.  With rows of 16 words the choices of a
+    // wavefront, random groups and one word of each, met at four banks: placing
+    // 131072 x 256, top-8, took 14.4 us instead of 13.4.
+    static constexpr int BS = LONG ? W + 4 : W, RS = W % 16 == 0 ? W + 8 : W;
+    __attribute__((aligned(16))) uint32_t bits[GROUPS * BS];
+    __attribute__((aligned(16))) uint16_t rank[LONG ? GROUPS * RS : 8];   // of a word's first bit
     int32_t first[LONG ? GROUPS + 1 : 1];                               // of a group, in the order of rows
     int32_t row[LONG ? H * NT : 1], token[LONG ? H * NT : 1];
     float weight[LONG ? H * NT : 1];
@@ -497,14 +507,15 @@ struct PlaceTable {
         return held < 32 * W ? held : 32 * W;
     }
     __device__ __forceinline__ void clear(const RouteArgs &a) {
-        for (int i = threadIdx.x; i < a.G * W; i += NT) bits[i] = 0;
+        for (int i = threadIdx.x; i < a.G * BS; i += NT) bits[i] = 0;
     }
 };
 // The table has been cleared, and a barrier passed since.
 template <int H, int NT, int W, int GROUPS>
 __device__ __forceinline__ void route_place(const RouteArgs &a, int64_t t0, int64_t t1, int32_t *base,
-                                            PlaceTable<H, NT, W, GROUPS> &tab, Choices<H> &c) {
+                                            PlaceTable<H, NT, W, GROUPS> &tab, Choices<H, NT> &c) {
     constexpr bool LONG = W >= 8;
+    constexpr int BS = PlaceTable<H, NT, W, GROUPS>::BS, RS = PlaceTable<H, NT, W, GROUPS>::RS;
     const int tid = threadIdx.x;
     const int step = tab.step(a);
     const int dq = NT / a.kk, dr = NT - dq * a.kk;
@@ -517,19 +528,22 @@ __device__ __forceinline__ void route_place(const RouteArgs &a, int64_t t0, int6
             for (int h = 0; h < H; h++) {
                 tok[h] = t;
                 const int g = c.group(h, n);
-                if (g >= 0) atomicOr(&tab.bits[g * W + (t >> 5)], 1u << (t & 31));
+                if (g >= 0) atomicOr(&tab.bits[g * BS + (t >> 5)], 1u << (t & 31));
                 t += dq + (r + dr >= a.kk ? 1 : 0);
                 r += dr - (r + dr >= a.kk ? a.kk : 0);
             }
         }
+        // All loads have arrived: below, waiting for one would wait for the stores before it as well.
+#pragma unroll
+        for (int h = 0; h < H; h++) asm volatile("" : "+v"(c.w[h]));
         __syncthreads();
         if constexpr (LONG) {
             for (int g = tid; g < a.G; g += NT) {
                 uint32_t k = 0;
 #pragma unroll
                 for (int x = 0; x < W; x += 8) {
-                    const uint4 lo = *reinterpret_cast<const uint4 *>(tab.bits + g * W + x);
-                    const uint4 hi = *reinterpret_cast<const uint4 *>(tab.bits + g * W + x + 4);
+                    const uint4 lo = *reinterpret_cast<const uint4 *>(tab.bits + g * BS + x);
+                    const uint4 hi = *reinterpret_cast<const uint4 *>(tab.bits + g * BS + x + 4);
                     const uint32_t b[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                     uint32_t r[4];
 #pragma unroll
@@ -538,12 +552,13 @@ __device__ __forceinline__ void route_place(const RouteArgs &a, int64_t t0, int6
                         r[y / 2] = k | (k1 << 16);
                         k = k1 + __popc(b[y + 1]);
                     }
-                    *reinterpret_cast<uint4 *>(tab.rank + g * W + x) = make_uint4(r[0], r[1], r[2], r[3]);
+                    *reinterpret_cast<uint4 *>(tab.rank + g * RS + x) = make_uint4(r[0], r[1], r[2], r[3]);
                 }
                 tab.first[g] = (int32_t)k;
             }
             __syncthreads();
-            exclusive_scan(tab.first, tab.first, a.G);
+            const int32_t rows = exclusive_scan<NT>(tab.first, a.G, [&](int g, int32_t sum) { tab.first[g] = sum; });
+            if (tid == 0) tab.first[a.G] = rows;
             __syncthreads();
         }
 #pragma unroll
@@ -551,10 +566,10 @@ __device__ __forceinline__ void route_place(const RouteArgs &a, int64_t t0, int6
             const int i = h * NT + tid, g = c.group(h, n), t = tok[h];
             int32_t p = -1;
             if (g >= 0) {
-                const uint32_t *b = tab.bits + g * W;
+                const uint32_t *b = tab.bits + g * BS;
                 int rank = __popc(b[t >> 5] & ((1u << (t & 31)) - 1u));
                 if constexpr (LONG) {
-                    rank += tab.rank[g * W + (t >> 5)];
+                    rank += tab.rank[g * RS + (t >> 5)];
                 } else {
                     for (int x = 0; x < W - 1; x++) rank += x < t >> 5 ? __popc(b[x]) : 0;
                 }
@@ -585,7 +600,7 @@ __device__ __forceinline__ void route_place(const RouteArgs &a, int64_t t0, int6
         s0 += step;
         __syncthreads();
         for (int i = tid; i < a.G; i += NT)
-            for (int x = 0; x < W; x++) base[i] += __popc(tab.bits[i * W + x]);
+            for (int x = 0; x < W; x++) base[i] += __popc(tab.bits[i * BS + x]);
         __syncthreads();
         tab.clear(a);
         __syncthreads();
@@ -599,11 +614,32 @@ __device__ void route_tail(const RouteArgs &a, int64_t used, int64_t i0, int64_t
     }
 }
 
-__device__ __forceinline__ void route_counts(const RouteArgs &a, const int32_t *tot, const int32_t *base) {
-    for (int i = threadIdx.x; i <= a.G; i += blockDim.x) {
-        a.counts[i] = tot[i];
-        a.off[i] = base[i];
+// Where the groups start, from the totals tot (LDS): counts and offsets for the
+// caller if `publish`, base[g] the start plus before[g] (LDS); returns the rows
+// in use.  The caller synchronizes.
+template <int NT>
+__device__ __forceinline__ int64_t route_offsets(const RouteArgs &a, const int32_t *tot, const int32_t *before,
+                                                 int32_t *base, bool publish) {
+    const int32_t used = exclusive_scan<NT>(tot, a.G, [&](int g, int32_t start) {
+        base[g] = start + (before ? before[g] : 0);
+        if (publish) {
+            a.counts[g] = tot[g];
+            a.off[g] = start;
+        }
+    });
+    if (publish && threadIdx.x == 0) {
+        a.counts[a.G] = tot[a.G];
+        a.off[a.G] = used;
     }
+    return used;
+}
+
+// Sum over four or eight neighbouring lanes, on all of them.
+template <int L>
+__device__ __forceinline__ int32_t lanes_sum(int32_t v) {
+    if (L == 8) v += __builtin_amdgcn_mov_dpp(v, DPP_MIRROR8, 0xF, 0xF, true);
+    v += __builtin_amdgcn_mov_dpp(v, DPP_XOR2, 0xF, 0xF, true);
+    return v + __builtin_amdgcn_mov_dpp(v, DPP_XOR1, 0xF, 0xF, true);
 }
 
 // First launch.  A batch of one run of at most ONE tokens is finished here, by
@@ -617,9 +653,9 @@ __global__ __launch_bounds__(BT) void k_route_select(RouteArgs a) {
     route_select<T, L, V, N, BT, VEC>(a, t0, t1, hist, psum);
     if constexpr (ONE > 0) {
         constexpr int H = 4;
-        __shared__ int32_t base[L * V + kMaxShared + 1];
+        __shared__ int32_t base[L * V + kMaxShared];
         __shared__ PlaceTable<H, BT, ONE / 32, L * V + kMaxShared> tab;
-        Choices<H> c;
+        Choices<H, BT> c;
         const int step = tab.step(a);
         c.load(a, 0, (int)(a.T < step ? a.T : step) * a.kk);
         tab.clear(a);
@@ -627,169 +663,219 @@ __global__ __launch_bounds__(BT) void k_route_select(RouteArgs a) {
             for (int e = tid; e < a.E; e += BT) a.prob_sum[e] = psum[e];
             if (tid < 64) route_loss(a, hist, psum);
         }
-        exclusive_scan(hist, base, a.G);
-        __syncthreads();
-        route_counts(a, hist, base);
-        const int64_t used = base[a.G];
+        const int64_t used = route_offsets<BT>(a, hist, nullptr, base, true);
         __syncthreads();
         route_place(a, 0, a.T, base, tab, c);
         route_tail(a, used, tid, BT);
     } else {
-        for (int i = tid; i < a.ldh; i += BT) {
-            const int h = i <= a.G ? hist[i] : 0;
-            if (a.CT > 255)
-                reinterpret_cast<uint16_t *>(a.hist)[((int64_t)(i / 8) * a.nwg + blockIdx.x) * 8 + i % 8] = (uint16_t)h;
-            else
-                reinterpret_cast<uint8_t *>(a.hist)[((int64_t)(i / 16) * a.nwg + blockIdx.x) * 16 + i % 16] = (uint8_t)h;
+        for (int i = tid; i <= a.G; i += BT) {
+            const int64_t at = (int64_t)i * a.ldh + blockIdx.x;
+            if (a.CT > 255) reinterpret_cast<uint16_t *>(a.hist)[at] = (uint16_t)hist[i];
+            else reinterpret_cast<uint8_t *>(a.hist)[at] = (uint8_t)hist[i];
         }
-        if (a.prob_sum)
+        if (a.prob_sum) {
+            if (blockIdx.x == 0 && tid == 0) *a.loss_sum = 0;
             for (int e = tid; e < a.lde; e += BT)
                 a.part[(int64_t)blockIdx.x * a.lde + e] = e < a.E ? psum[e] : 0.0f;
+        }
     }
 }
 
 // Sums over all runs, and over the runs before run b, of the histograms'
-// columns into tot and before (LDS [ldh]).  A row of 16 lanes takes a piece, a
-// lane every 16th run with 16 in flight (a batch of 256 runs and up to 512
-// bytes of counts is one round trip), and the lanes are added by DPP; adding
-// partial sums by LDS atomics took twice the time of everything else here.
-// u8 counts are added as pairs of 16 bits: a column's total is at most
-// T <= 256 * 255.
+// columns [c0, c0 + n) and G into tot and before (LDS [n + 1]).  Four (u16: eight) lanes take a
+// column, 256 runs of it in flight (a batch has no more up to 16.7 million
+// tokens) and the next column's behind them.  A word of a column is four (u16: two) runs, so one dot
+// product adds them to the total and one, with weights that end at run b, to
+// what precedes it: 2 instructions for 4 counts.  With the columns of a run side
+// by side, masked and added as pairs of 16 bits (10 instructions for 4 counts),
+// the sums took 7100 cycles for 257 columns and 10900 for 513.
 template <typename HT, int NT>
-__device__ __forceinline__ void route_totals(const RouteArgs &a, int b, int32_t *tot, int32_t *before) {
-    constexpr int P = 16 / sizeof(HT), U = 16;
-    const int lane = threadIdx.x & 15;
-    for (int q = threadIdx.x >> 4; q < a.ldh / P; q += NT / 16) {
-        const uint4 *x = reinterpret_cast<const uint4 *>(a.hist) + (int64_t)q * a.nwg;
-        uint32_t s[8], sb[8];                    // words of two 16-bit counts (u8), or counts
+__device__ __forceinline__ void route_totals(const RouteArgs &a, int b, int c0, int n, int32_t *tot, int32_t *before) {
+    constexpr int SZ = (int)sizeof(HT), PW = 4 / SZ, L = 4 * SZ, U = 4, RUNS = 256;
+    const auto weights = [](int n) -> uint32_t {   // 1 for the first n runs of a word
+        const uint32_t one = SZ == 1 ? 0x01010101u : 0x00010001u;
+        return n <= 0 ? 0u : n >= PW ? one : one & ((1u << (8 * SZ * n)) - 1u);
+    };
+    const auto dot = [](uint32_t x, uint32_t w, uint32_t s) -> uint32_t {
+        if constexpr (SZ == 1) {
+            return __builtin_amdgcn_udot4(x, w, s, false);
+        } else {
+            typedef unsigned short u16v2 __attribute__((ext_vector_type(2)));
+            return __builtin_amdgcn_udot2(__builtin_bit_cast(u16v2, x), __builtin_bit_cast(u16v2, w), s, false);
+        }
+    };
+    const int lane = threadIdx.x & (L - 1), q0 = threadIdx.x / L;
+    const auto pass = [&](int r0) {
+        uint32_t all[4 * U], pre[4 * U];
 #pragma unroll
-        for (int i = 0; i < 8; i++) s[i] = sb[i] = 0;
-        for (int w0 = lane; w0 < a.nwg; w0 += 16 * U) {
+        for (int i = 0; i < 4 * U; i++) {
+            const int r = r0 + ((i / 4) * L + lane) * 4 * PW + i % 4 * PW;
+            all[i] = weights(a.nwg - r);
+            pre[i] = weights(b - r);
+        }
+        const auto load = [&](int q, uint4 (&h)[U]) {
+            const uint4 *x = reinterpret_cast<const uint4 *>(
+                reinterpret_cast<const HT *>(a.hist) + (int64_t)(q < n ? c0 + q : a.G) * a.ldh + r0) + lane;
+#pragma unroll
+            for (int u = 0; u < U; u++) h[u] = x[r0 + 64 * u < a.ldh ? L * u : 0];
+        };
+        uint4 next[U];
+        load(q0, next);
+        for (int q = q0; q <= n; q += NT / L) {
             uint4 h[U];
 #pragma unroll
-            for (int u = 0; u < U; u++) h[u] = x[w0 + 16 * u < a.nwg ? w0 + 16 * u : 0];
+            for (int u = 0; u < U; u++) h[u] = next[u];
+            if (q + NT / L <= n) load(q + NT / L, next);
+            uint32_t s[4] = {0, 0, 0, 0}, sb[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                const uint32_t all = w0 + 16 * u < a.nwg ? ~0u : 0u, m = w0 + 16 * u < b ? ~0u : 0u;
-                const uint32_t v[4] = {h[u].x & all, h[u].y & all, h[u].z & all, h[u].w & all};
+                const uint32_t w[4] = {h[u].x, h[u].y, h[u].z, h[u].w};
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const uint32_t even = sizeof(HT) == 1 ? v[i] & 0x00FF00FFu : v[i] & 0xFFFFu;
-                    const uint32_t odd = sizeof(HT) == 1 ? (v[i] >> 8) & 0x00FF00FFu : v[i] >> 16;
-                    s[2 * i] += even;
-                    s[2 * i + 1] += odd;
-                    sb[2 * i] += even & m;
-                    sb[2 * i + 1] += odd & m;
+                    s[i] = dot(w[i], all[4 * u + i], s[i]);
+                    sb[i] = dot(w[i], pre[4 * u + i], sb[i]);
                 }
             }
+            const int32_t v = lanes_sum<L>((int32_t)(s[0] + s[1] + s[2] + s[3]));
+            const int32_t vb = lanes_sum<L>((int32_t)(sb[0] + sb[1] + sb[2] + sb[3]));
+            if (lane == 0) tot[q] = (r0 ? tot[q] : 0) + v;
+            if (lane == 1) before[q] = (r0 ? before[q] : 0) + vb;
         }
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            s[i] = row_sum(s[i]);
-            sb[i] = row_sum(sb[i]);
-        }
-        // every lane has the sums: lane c of the row writes column c
-        if (lane < P) {
-            uint32_t v = 0, vb = 0;
-            const int i = sizeof(HT) == 1 ? 2 * (lane / 4) + lane % 2 : lane;   // u8: byte lane % 4 of word lane / 4
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                v = i == k ? s[k] : v;
-                vb = i == k ? sb[k] : vb;
-            }
-            const int sh = 16 * ((lane % 4) / 2);
-            tot[P * q + lane] = (int32_t)(sizeof(HT) == 1 ? (v >> sh) & 0xFFFFu : v);
-            before[P * q + lane] = (int32_t)(sizeof(HT) == 1 ? (vb >> sh) & 0xFFFFu : vb);
-        }
-    }
+    };
+    pass(0);   // out of the loop, whose head would wait for the caller's loads
+    for (int r0 = RUNS; r0 < a.nwg; r0 += RUNS) pass(r0);
     __syncthreads();
 }
 
-// Second launch: workgroup b < nwg places the rows of its run; the last one of
-// the grid sums the probabilities.  Every workgroup adds up the histograms of all runs
-// by itself (what precedes its run, and the totals): about 256 rows of G + 1
-// bytes (or 2-byte words) from L2, which is less than a third launch costs.
+// The sums of the probabilities over the runs and the loss.  Workgroup i takes
+// the quads of experts [i S, +S), S = a.slice; 64 / S runs are on a wavefront.
+// Eight workgroups, beside those that place the rows: one alone was the last to
+// finish by 3.4 us for 256 runs of 256 experts and by 16 for 1000.  Their parts
+// of the loss, at most 1 together, meet in one 64-bit integer: 46 bits of the
+// sum in units of 2^-44, then how many parts are NaN, then how many have been
+// added, 9 bits each.  An integer sum has no order, and whoever's addition is
+// the last has the whole loss in hand without reading what others stored
+// (storing the parts and counting them with release and acquire took 3.5 us).
+// The loss is at least about k / E of its scale, so eight parts rounded to
+// 2^-44 are finer than f32.  tot, scratch: LDS
+// [4 S + 1]; red: LDS [NT / 64][S].
+template <typename HT, int NT>
+__device__ __forceinline__ void route_sums(const RouteArgs &a, int i, int32_t *tot, int32_t *scratch, float4 *red) {
+    constexpr int U = 4;
+    const int S = a.slice, quads = a.lde / 4, q0 = i * S;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = threadIdx.x & (S - 1), q = q0 + col < quads ? q0 + col : 0;
+    const float4 *x = reinterpret_cast<const float4 *>(a.part) + q;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int w = threadIdx.x / S; w < a.nwg; w += U * (NT / S)) {
+        float4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) v[u] = x[(int64_t)(w + u * (NT / S) < a.nwg ? w + u * (NT / S) : 0) * quads];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const bool in = w + u * (NT / S) < a.nwg;
+            s.x += in ? v[u].x : 0.0f;
+            s.y += in ? v[u].y : 0.0f;
+            s.z += in ? v[u].z : 0.0f;
+            s.w += in ? v[u].w : 0.0f;
+        }
+    }
+    for (int o = 32; o >= S; o >>= 1) {
+        s.x += __shfl_xor(s.x, o, 64);
+        s.y += __shfl_xor(s.y, o, 64);
+        s.z += __shfl_xor(s.z, o, 64);
+        s.w += __shfl_xor(s.w, o, 64);
+    }
+    if (lane < S) red[wave * S + lane] = s;
+    const int n = a.E - 4 * q0 < 4 * S ? a.E - 4 * q0 : 4 * S;   // experts
+    route_totals<HT, NT>(a, 0, 4 * q0, n, tot, scratch);
+    if (wave != 0) return;
+    float loss = 0.0f;
+    if (4 * lane < n) {
+        s = red[lane];
+        for (int w = 1; w < NT / 64; w++) {
+            const float4 v = red[w * S + lane];
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int e = 4 * (q0 + lane) + j;
+            if (e < a.E) {
+                a.prob_sum[e] = v[j];
+                loss += loss_term(tot[4 * lane + j], v[j], tot[n]);
+            }
+        }
+    }
+    loss = wave_sum(loss);
+    if (lane != 0) return;
+    const uint64_t mine = (1ull << 55) | (loss == loss ? (uint64_t)(loss * 0x1p44f) : 1ull << 46);
+    const uint64_t all =
+        mine + __hip_atomic_fetch_add(a.loss_sum, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if ((int)(all >> 55) != (quads + S - 1) / S) return;
+    const float sum = (float)(all & ((1ull << 46) - 1)) * 0x1p-44f;
+    *a.loss = (all >> 46) & 511 ? NAN : sum * ((float)a.E / (float)a.k);
+}
+
+// Second launch: workgroup b < nwg places the rows of its run, those after them
+// sum the probabilities.  Every workgroup adds up the histograms of all runs by
+// itself (what precedes its run, and the totals): about 256 bytes or 2-byte
+// words for each of G + 1 columns from L2, which is less than a third launch
+// costs.
 template <typename HT, int NT, int W, int GROUPS>
 __global__ __launch_bounds__(NT, 4) void k_route_place(RouteArgs a) {
     constexpr int H = 4;
-    __shared__ int32_t tot[GROUPS + 16], before[GROUPS + 16], base[GROUPS + 1];
+    __shared__ int32_t tot[GROUPS + 1], before[GROUPS + 1], base[GROUPS];
     __shared__ PlaceTable<H, NT, W, GROUPS> tab;
-    __shared__ __attribute__((aligned(16))) float red[4 * NT];
     const int tid = threadIdx.x, b = blockIdx.x;
+    if (b >= a.nwg) {
+        __shared__ float4 red[NT / 64 * kMaxSlice];
+        route_sums<HT, NT>(a, b - a.nwg, tot, before, red);
+        return;
+    }
     const int64_t t0 = (int64_t)b * a.CT, t1 = t0 + a.CT < a.T ? t0 + a.CT : a.T;
-    Choices<H> c;
-    if (b < a.nwg) {
-        const int step = tab.step(a);
-        c.load(a, t0, (int)(t1 - t0 < step ? t1 - t0 : step) * a.kk);
-        tab.clear(a);
-    }
-    route_totals<HT, NT>(a, b, tot, before);
-    if (b < a.nwg) {
-        exclusive_scan(tot, base, a.G);   // group starts; base[G] is the rows in use
-        __syncthreads();
-        const int64_t used = base[a.G];
-        if (b == 0) {
-            route_counts(a, tot, base);
-            __syncthreads();
-        }
-        for (int i = tid; i < a.G; i += NT) base[i] += before[i];
-        __syncthreads();
-        route_place(a, t0, t1, base, tab, c);
-        route_tail(a, used, (int64_t)b * NT + tid, (int64_t)a.nwg * NT);
-    }
-    if (!a.prob_sum || b != (int)gridDim.x - 1) return;
-    // the loss, by a workgroup of its own or the last run's
-    const int quads = a.lde / 4, parts = NT / quads, part = tid / quads, q = tid % quads;
-    if (part < parts) {
-        constexpr int U = 4;
-        const float4 *x = reinterpret_cast<const float4 *>(a.part);
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int w = part; w < a.nwg; w += U * parts) {
-            float4 v[U];
-#pragma unroll
-            for (int u = 0; u < U; u++) v[u] = x[(int64_t)(w + u * parts < a.nwg ? w + u * parts : 0) * quads + q];
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                const bool in = w + u * parts < a.nwg;
-                s.x += in ? v[u].x : 0.0f;
-                s.y += in ? v[u].y : 0.0f;
-                s.z += in ? v[u].z : 0.0f;
-                s.w += in ? v[u].w : 0.0f;
-            }
-        }
-        reinterpret_cast<float4 *>(red)[part * quads + q] = s;   // [parts][lde]
-    }
+    Choices<H, NT> c;
+    const int step = tab.step(a);
+    c.load(a, t0, (int)(t1 - t0 < step ? t1 - t0 : step) * a.kk);
+    tab.clear(a);
+    route_totals<HT, NT>(a, b, 0, a.G, tot, before);
+    const int64_t used = route_offsets<NT>(a, tot, before, base, b == 0);
     __syncthreads();
-    float *sum = reinterpret_cast<float *>(before);              // of use to nobody any more
-    for (int e = tid; e < a.E; e += NT) {
-        float s = 0.0f;
-        for (int w = 0; w < parts; w++) s += red[w * a.lde + e];
-        sum[e] = s;
-        a.prob_sum[e] = s;
-    }
-    __syncthreads();
-    if (tid < 64) route_loss(a, tot, sum);
+    route_place(a, t0, t1, base, tab, c);
+    route_tail(a, used, (int64_t)b * NT + tid, (int64_t)a.nwg * NT);
 }
 
 static int32_t round_up(int64_t n, int64_t m) { return (int32_t)((n + m - 1) / m * m); }
 
 // Runs of whole words of tokens, about one to a compute unit (the placing reads
-// every run's histogram in every workgroup), with counts below 2^16.
-static void route_runs(int64_t T, int64_t E, int64_t k, int32_t &CT, int32_t &nwg) {
+// every run's histogram in every workgroup), with counts below 2^16.  Where a
+// compute unit holds one workgroup of the placing, eight are left to the sums.
+static void route_runs(int64_t T, int64_t E, int64_t k, int64_t shared, int32_t &CT, int32_t &nwg) {
     const int64_t one = k <= 8 && E <= 256 ? kOneLargeTokens : kOneSmallTokens;
-    CT = T <= one ? (int32_t)one : T >= 256 * 65504ll ? 65504 : round_up((T + 255) / 256, 32);
+    CT = T <= one ? (int32_t)one : T >= 248 * 65504ll ? 65504 : round_up((T + 255) / 256, 32);
+    if (T > one && T < 248 * 65504ll && (CT > 255 || (CT > 32 && E + shared > kFewGroups)))
+        CT = round_up((T + 255 - kSums) / (256 - kSums), 32);
     nwg = (int32_t)((T + CT - 1) / CT);
 }
 
+// Runs from one column of the histograms to the next: what four lanes (of two
+// bytes: eight) load at a time.
+static int32_t hist_stride(int32_t nwg) { return round_up(nwg, 64); }
+
 int64_t route_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t shared) {
     int32_t CT, nwg;
-    route_runs(T, E, k, CT, nwg);
-    return nwg == 1 ? 0 : (int64_t)nwg * ((CT > 255 ? 2 : 1) * round_up(E + shared + 1, 16) + 4 * round_up(E, 4));
+    route_runs(T, E, k, shared, CT, nwg);
+    if (nwg == 1) return 0;
+    return (E + shared + 1) * hist_stride(nwg) * (CT > 255 ? 2 : 1) + 4ll * nwg * round_up(E, 4) + 8;
 }
 
 template <typename T, int L, int V, int N, bool VEC>
 static void route_launch_few(const RouteArgs &a, hipStream_t s) {
-    constexpr int B = N == 8 && L > 8 && L * V <= 512 ? 512 : 256;
+    // threads: 8192 x 512 13.2 us with 256, 10.9 with 512; the longer lists need the registers
+    constexpr int B = N == 8 ? 512 : 256;
     if (a.T <= kOneSmallTokens) {
         k_route_select<T, L, V, N, 256, kOneSmallTokens, VEC><<<1, 256, 0, s>>>(a);
     } else if (a.nwg > 1) {
@@ -805,13 +891,16 @@ static void route_few(const RouteArgs &a, hipStream_t s) {
     else if (a.k <= 16) route_launch_few<T, L, V, 16, VEC>(a, s);
     else route_launch_few<T, L, V, 32, VEC>(a, s);
 }
+// Lanes and logits to a lane, f32, choice of 8192 tokens: 64 experts 4.7 us with
+// 8 x 8 and 5.2 with 16 x 4; 128: 5.2 with 8 x 16, 5.6 with 16 x 8; 256: 6.7 with
+// 16 x 16, 8.3 with 32 x 8; 512: 10.0 with 16 x 32, 10.9 with 32 x 16 (65536
+// tokens: 36.8 and 51.4).
 template <typename T, bool VEC>
 static void route_few_experts(const RouteArgs &a, hipStream_t s) {
-    constexpr int Q = kPiece<T>;
-    if (a.E <= 64) route_few<T, 64 / Q, Q, VEC>(a, s);
+    if (a.E <= 64) route_few<T, 8, 8, VEC>(a, s);
     else if (a.E <= 128) route_few<T, 8, 16, VEC>(a, s);
     else if (a.E <= 256) route_few<T, 16, 16, VEC>(a, s);
-    else if (a.E <= 512) route_few<T, 32, 16, VEC>(a, s);
+    else if (a.E <= 512) route_few<T, 16, 32, VEC>(a, s);
     else route_few<T, 32, 32, VEC>(a, s);
 }
 
@@ -841,12 +930,10 @@ static void route_dispatch(const RouteArgs &a, bool vec, hipStream_t s) {
         route_few_experts<T, false>(a, s);
     }
     if (a.nwg == 1) return;
-    // The loss has a workgroup of its own, except beside 1024-thread workgroups,
-    // of which a compute unit holds one: 257 of them would be two rounds.
-    const unsigned grid = (unsigned)(a.nwg + (a.prob_sum && a.CT <= 255 ? 1 : 0));
+    const unsigned grid = (unsigned)(a.nwg + (a.prob_sum ? (a.lde / 4 + a.slice - 1) / a.slice : 0));
     if (a.CT > 255) {
-        if (a.G <= kFewGroups) k_route_place<uint16_t, 1024, 16, kFewGroups><<<a.nwg, 1024, 0, s>>>(a);
-        else k_route_place<uint16_t, 1024, 8, kMaxGroups><<<a.nwg, 1024, 0, s>>>(a);
+        if (a.G <= kFewGroups) k_route_place<uint16_t, 1024, 16, kFewGroups><<<grid, 1024, 0, s>>>(a);
+        else k_route_place<uint16_t, 1024, 8, kMaxGroups><<<grid, 1024, 0, s>>>(a);
     } else if (a.CT > 32) {
         if (a.G <= kFewGroups) k_route_place<uint8_t, 512, 8, kFewGroups><<<grid, 512, 0, s>>>(a);
         else k_route_place<uint8_t, 512, 8, kMaxGroups><<<grid, 512, 0, s>>>(a);
@@ -872,12 +959,15 @@ hipError_t launch_route(const void *logits, int dtype, int64_t T, int64_t E, int
     const bool vec = whole_pieces(E, ldl, dtype);
     a.experts = experts; a.counts = counts; a.src = src; a.pos = pos;
     a.weights = weights; a.row_weights = row_weights; a.prob_sum = prob_sum; a.loss = loss; a.off = off;
-    route_runs(T, E, k, a.CT, a.nwg);
-    a.ldh = round_up(E + shared + 1, 16);
+    route_runs(T, E, k, shared, a.CT, a.nwg);
+    a.ldh = hist_stride(a.nwg);
     a.lde = round_up(E, 4);
     a.hist = workspace;
     a.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) +
-                                       (int64_t)a.nwg * a.ldh * (a.CT > 255 ? 2 : 1));
+                                       (int64_t)(a.G + 1) * a.ldh * (a.CT > 255 ? 2 : 1));
+    a.loss_sum = reinterpret_cast<uint64_t *>(a.part + (int64_t)a.nwg * a.lde);
+    a.slice = 1;
+    while (a.slice * kSums < a.lde / 4) a.slice *= 2;
     if (dtype == BSP_DTYPE_BF16) route_dispatch<uint16_t>(a, vec, s);
     else route_dispatch<float>(a, vec, s);
     return hipGetLastError();
