@@ -143,7 +143,7 @@ __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt(const T *__restrict__ h1
                                                      uint8_t *__restrict__ ckpt_scales) {
     constexpr int VE = kVE<T>;
     const int lane = threadIdx.x & (LPR - 1);
-    const int64_t r = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const int64_t r = grid_index() * (256 / LPR) + threadIdx.x / LPR;
     if (r >= R) return;
     const bool used = !n_rows || r < *n_rows;
     const float w = used && row_weights ? row_weights[r] : 1.0f;
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt_bwd(const T *__restrict_
                                                          float *__restrict__ d_row_weights) {
     constexpr int VE = kVE<T>;
     const int lane = threadIdx.x & (LPR - 1);
-    const int64_t r = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const int64_t r = grid_index() * (256 / LPR) + threadIdx.x / LPR;
     if (r >= R) return;
     const bool used = !n_rows || r < *n_rows;
     const float w = used && row_weights ? row_weights[r] : 1.0f;
@@ -247,7 +247,7 @@ static void ckpt_launch(const void *h13, int64_t R, int64_t I, const float *row_
                         hipStream_t s) {
     with_lanes<T>(R, I, [&](auto l, auto nt) {
         constexpr int LPR = decltype(l)::value, RW = 256 / LPR;
-        k_swiglu_ckpt<T, LPR, decltype(nt)::value><<<(unsigned)((R + RW - 1) / RW), 256, 0, s>>>(
+        k_swiglu_ckpt<T, LPR, decltype(nt)::value><<<grid_of((R + RW - 1) / RW), 256, 0, s>>>(
             reinterpret_cast<const T *>(h13), R, I, row_weights, n_rows, h_out, codes, scales, ckpt_codes, ckpt_scales);
     });
 }
@@ -258,7 +258,7 @@ static void ckpt_bwd_launch(const void *dh, int64_t R, int64_t I, const uint8_t 
                             uint16_t *h_out, float *d_row_weights, hipStream_t s) {
     with_lanes<T>(R, I, [&](auto l, auto nt) {
         constexpr int LPR = decltype(l)::value, RW = 256 / LPR;
-        k_swiglu_ckpt_bwd<T, LPR, decltype(nt)::value><<<(unsigned)((R + RW - 1) / RW), 256, 0, s>>>(
+        k_swiglu_ckpt_bwd<T, LPR, decltype(nt)::value><<<grid_of((R + RW - 1) / RW), 256, 0, s>>>(
             reinterpret_cast<const T *>(dh), R, I, ckpt_codes, ckpt_scales, row_weights, n_rows,
             reinterpret_cast<T *>(dh13), h_out, d_row_weights);
     });

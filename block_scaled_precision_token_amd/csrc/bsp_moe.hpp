@@ -28,6 +28,14 @@ hipError_t launch_swiglu_checkpoint_backward(const void *dh, int dtype, int64_t 
                                              const float *row_weights, const int64_t *n_rows, void *dh13,
                                              uint16_t *h_out, float *d_row_weights, hipStream_t s);
 
+// A row of n workgroups as a grid: a grid dimension holds fewer than 2^32
+// threads, so longer rows go on over y; the last may be partly past n.
+constexpr int64_t kGridX = 1ll << 23;   // of at most 256 threads
+inline dim3 grid_of(int64_t n) {
+    return n <= kGridX ? dim3((unsigned)n) : dim3((unsigned)kGridX, (unsigned)((n + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ int64_t grid_index() { return blockIdx.y * kGridX + blockIdx.x; }
+
 // ---- device helpers shared by the kernels of these entry points ----
 
 // Sum over the 64 lanes, the same bits on every lane.

@@ -18,7 +18,9 @@ constexpr float kLog2e = 1.44269504088896341f;
 // instead of 6.7 for 64 experts and 9.4 instead of 10.2 for 256 (the same for
 // 128), 24000 tokens 6.2 / 8.6 and 10.1 / 12.2; below, 4096 x 128 6.4 instead of 5.1.
 constexpr int64_t kManyTokens = 16384;
-constexpr int64_t kBwdWorkgroups = 768;   // three to a compute unit, as the registers of the widest form allow
+// Gradient: three workgroups to a compute unit, as the registers of the widest
+// form allow (65537 x 256 bf16: 19.7 us, with 1536 22.8).
+constexpr int64_t kBwdWorkgroups = 768;
 // Batches that one workgroup finishes in one launch: of 256 threads, or of 1024
 // for up to 256 experts and k <= 8 (128 tokens, 128 experts: 10.5 us a call
 // instead of 15.3 with two launches; 256 tokens: 14.5, and 24 with 256 experts).
@@ -992,10 +994,14 @@ struct RouteBwdArgs {
     const float *d_weights, *d_loss;
 };
 
-// Per element the terms that every expert has are one multiply-add of the
-// count and one product, e (c1 f - c2); the k chosen experts' own terms are
-// added by the lane that holds the choice: it evaluates its logit again and
-// stores over the row's element (the same wavefront's store, issued later).
+// Bound by HBM, every logit read and written once (8192 x 128 f32 4.8 us; 65537 x
+// 256 bf16 19.7 us, 3.8 TB/s): a wavefront's loads of a token's logits and choices
+// go out together, then the gathers by the choice, and loading the next token's
+// ahead of them gained nothing.  Per element the terms that every expert has are
+// one multiply-add of the count and one product, e (c1 f - c2); the k chosen
+// experts' own terms are added by the lane that holds the choice: it evaluates
+// its logit again and stores over the row's element (the same wavefront's store,
+// issued later).
 template <typename T, int L, int V, bool VEC>
 __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
     constexpr int KS = 32 / L;                // choices per lane, k <= 32
@@ -1079,14 +1085,18 @@ static void route_bwd_launch(const RouteBwdArgs &a, hipStream_t s) {
     const unsigned grid = (unsigned)(wgs < kBwdWorkgroups ? wgs : kBwdWorkgroups);
     k_route_bwd<T, L, V, VEC><<<grid, 256, 0, s>>>(a);
 }
+// Lanes and logits to a lane: 128 experts 8 x 16 (65536 tokens f32: 16.1 us, 16 x 8
+// 17.3, 4 x 32 19.3; 32768 bf16: 9.0, 10.4, 9.5); 256 experts 16 x 16, in bf16 and
+// with many tokens 8 x 32 (65537 bf16: 19.7 instead of 21.4; but 20000 f32 12.8
+// instead of 11.8, and 4096 f32 5.4 instead of 5.0); 512 experts 32 x 16 (65536
+// f32: 53.8, 16 x 32 58.2).
 template <typename T, bool VEC>
 static void route_bwd_dispatch(const RouteBwdArgs &a, hipStream_t s) {
     constexpr int Q = kPiece<T>;
-    const bool many = a.T >= kManyTokens;
+    const bool many = Q == 8 && a.T >= kManyTokens;
     if (a.E <= 64) route_bwd_launch<T, 64 / Q, Q, VEC>(a, s);
-    else if (a.E <= 128 && many) route_bwd_launch<T, 4, 32, VEC>(a, s);
-    else if (a.E <= 128) route_bwd_launch<T, 16, 8, VEC>(a, s);
-    else if (a.E <= 256 && many) route_bwd_launch<T, 8, 32, VEC>(a, s);
+    else if (a.E <= 128) route_bwd_launch<T, 8, 16, VEC>(a, s);
+    else if (a.E <= 256 && many) route_bwd_launch<T, Q == 8 ? 8 : 16, Q == 8 ? 32 : 16, VEC>(a, s);
     else if (a.E <= 256) route_bwd_launch<T, 16, 16, VEC>(a, s);
     else if (a.E <= 512) route_bwd_launch<T, 32, 16, VEC>(a, s);
     else route_bwd_launch<T, 32, 32, VEC>(a, s);
@@ -1153,7 +1163,7 @@ __global__ __launch_bounds__(256) void k_combine(const TI *__restrict__ y, int64
                                                  const int32_t *__restrict__ pos, const float *__restrict__ weights,
                                                  int64_t T, int kk, int nc, TO *__restrict__ out, int64_t ldo) {
     constexpr int VE = 16 / (int)sizeof(TI);
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = grid_index() * 256 + threadIdx.x;
     const int64_t t = i / nc;
     if (t >= T) return;
     const int c = (int)(i - t * nc) * VE;
@@ -1185,7 +1195,7 @@ template <typename TI, typename TO>
 static void combine_launch(const void *y, int64_t rows, int64_t H, int64_t ldy, const int32_t *pos,
                            const float *weights, int64_t T, int64_t kk, void *out, int64_t ldo, hipStream_t s) {
     const int64_t nc = H * (int64_t)sizeof(TI) / 16, n = T * nc;
-    k_combine<TI, TO><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(reinterpret_cast<const TI *>(y), rows, ldy, pos,
+    k_combine<TI, TO><<<grid_of((n + 255) / 256), 256, 0, s>>>(reinterpret_cast<const TI *>(y), rows, ldy, pos,
                                                                  weights, T, (int)kk, (int)nc,
                                                                  reinterpret_cast<TO *>(out), ldo);
 }
