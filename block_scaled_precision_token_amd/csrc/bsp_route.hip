@@ -644,7 +644,8 @@ __device__ __forceinline__ int32_t lanes_sum(int32_t v) {
     return v + __builtin_amdgcn_mov_dpp(v, DPP_XOR1, 0xF, 0xF, true);
 }
 
-// First launch.  A batch of one run of at most ONE tokens is finished here, by
+// First launch, bound by the vector units (8192 x 128 5.4 us, 100003 x 96 14.4 us,
+// of which 7.9 are the issue of its vector instructions).  A batch of one run of at most ONE tokens is finished here, by
 // its one workgroup (ONE = 0: there are more runs).
 template <typename T, int L, int V, int N, int BT, int ONE, bool VEC>
 __global__ __launch_bounds__(BT) void k_route_select(RouteArgs a) {
@@ -826,7 +827,8 @@ __device__ __forceinline__ void route_sums(const RouteArgs &a, int i, int32_t *t
 // sum the probabilities.  Every workgroup adds up the histograms of all runs by
 // itself (what precedes its run, and the totals): about 256 bytes or 2-byte
 // words for each of G + 1 columns from L2, which is less than a third launch
-// costs.
+// costs.  Bound by the latency of its phases: 8192 x 128 5.8 us, 8192 x 512 6.6,
+// 100003 x 96 8.6, of which the histograms' round trip and sums are about 2.
 template <typename HT, int NT, int W, int GROUPS>
 __global__ __launch_bounds__(NT, 4) void k_route_place(RouteArgs a) {
     constexpr int H = 4;
