@@ -754,13 +754,13 @@ __device__ __forceinline__ void route_totals(const RouteArgs &a, int b, int c0, 
 // the quads of experts [i S, +S), S = a.slice; 64 / S runs are on a wavefront.
 // Eight workgroups, beside those that place the rows: one alone was the last to
 // finish by 3.4 us for 256 runs of 256 experts and by 16 for 1000.  Their parts
-// of the loss, at most 1 together, meet in one 64-bit integer: 46 bits of the
-// sum in units of 2^-44, then how many parts are NaN, then how many have been
-// added, 9 bits each.  An integer sum has no order, and whoever's addition is
+// of the loss, at most 1 together, meet in one 64-bit integer: 56 bits of the
+// sum in units of 2^-54, then how many parts are NaN, then how many have been
+// added, 4 bits each.  An integer sum has no order, and whoever's addition is
 // the last has the whole loss in hand without reading what others stored
 // (storing the parts and counting them with release and acquire took 3.5 us).
-// The loss is at least about k / E of its scale, so eight parts rounded to
-// 2^-44 are finer than f32.  tot, scratch: LDS
+// The sum is at least 1 / E^2 (a token's largest probability is at least 1 / E),
+// so eight parts rounded to 2^-54 are finer than f32.  tot, scratch: LDS
 // [4 S + 1]; red: LDS [NT / 64][S].
 template <typename HT, int NT>
 __device__ __forceinline__ void route_sums(const RouteArgs &a, int i, int32_t *tot, int32_t *scratch, float4 *red) {
@@ -815,12 +815,12 @@ __device__ __forceinline__ void route_sums(const RouteArgs &a, int i, int32_t *t
     }
     loss = wave_sum(loss);
     if (lane != 0) return;
-    const uint64_t mine = (1ull << 55) | (loss == loss ? (uint64_t)(loss * 0x1p44f) : 1ull << 46);
+    const uint64_t mine = (1ull << 60) | (loss == loss ? (uint64_t)(loss * 0x1p54f) : 1ull << 56);
     const uint64_t all =
         mine + __hip_atomic_fetch_add(a.loss_sum, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if ((int)(all >> 55) != (quads + S - 1) / S) return;
-    const float sum = (float)(all & ((1ull << 46) - 1)) * 0x1p-44f;
-    *a.loss = (all >> 46) & 511 ? NAN : sum * ((float)a.E / (float)a.k);
+    if ((int)(all >> 60) != (quads + S - 1) / S) return;
+    const float sum = (float)(all & ((1ull << 56) - 1)) * 0x1p-54f;
+    *a.loss = (all >> 56) & 15 ? NAN : sum * ((float)a.E / (float)a.k);
 }
 
 // Second launch: workgroup b < nwg places the rows of its run, those after them
