@@ -114,13 +114,41 @@ __device__ __forceinline__ void mx_values(const Codes<VE> &c, uint32_t sc, float
     }
 }
 
-// 1 / (1 + exp(-z)).  Evaluated as 2^-32 / (2^-32 + 2^(-z log2(e) - 32)):
-// V_RCP_F32 flushes results below 2^-126 to zero, which the plain form meets
-// from z < -87.3 while z s is still above the smallest bf16 values; the factor
-// keeps its argument and result normal down to z = -110.
-__device__ __forceinline__ float sigmoid(float z) {
-    const float e = __builtin_amdgcn_exp2f(fmaf(z, -1.44269504088896341f, -32.0f));
-    return __builtin_amdgcn_rcpf(0x1p-32f + e) * 0x1p-32f;
+// s = 1 / (1 + e), e = exp(-z), and (FULL) c = 1 - s = e s, of VE values.
+// FULL, for f32 results: e = 2^t (1 + d), t = -z log2(e) rounded and d what the
+// rounding left out; without d the error of e grows with |z| (2.8 units of 2^-24
+// at 4, 60 at 80).  With it s is within 6 + 0.05 |z| units and c, which 1 - s
+// would cancel, within 10 + 0.1 |z|.  The forward's h is rounded to bf16 and does
+// without.  Past |z| = 87 2^t, the reciprocal (V_RCP_F32 flushes results below
+// 2^-126) and d run out of range; a wavefront that has such a value takes exp(z)
+// for s there, scaled by 2^64 until the end: subnormal from -87.3, 0 below -104.
+template <bool FULL, int VE>
+__device__ __forceinline__ void sigmoid(const float (&z)[VE], float (&s)[VE], float (&c)[VE]) {
+    constexpr float L2E = 1.44269504088896341f, LN2 = 0.693147180559945309f, FAR = 87.0f;
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VE; i++) {
+        const float t = z[i] * -L2E;
+        float e = __builtin_amdgcn_exp2f(t);
+        if (FULL) e = fmaf(e, fmaf(-t, LN2, -z[i]), e);
+        s[i] = __builtin_amdgcn_rcpf(1.0f + e);
+        c[i] = e * s[i];
+        top = fmaxf(top, fabsf(z[i]));
+    }
+    if (__any(top > FAR)) {
+#pragma unroll
+        for (int i = 0; i < VE; i++) {
+            const float x = fmaxf(z[i], -110.0f), t = x * L2E;
+            const float e = __builtin_amdgcn_exp2f(t + 64.0f);
+            if (z[i] < -FAR) {
+                s[i] = fmaf(e, fmaf(-t, LN2, x), e) * 0x1p-64f;
+                c[i] = 1.0f;
+            } else if (z[i] > FAR) {
+                s[i] = 1.0f;
+                c[i] = 0.0f;
+            }
+        }
+    }
 }
 
 // Sum over LPR neighbouring lanes, the same bits on each.
@@ -165,8 +193,10 @@ __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt(const T *__restrict__ h1
             ckpt_scales[at / 32] = (uint8_t)sg;
             ckpt_scales[(at + I) / 32] = (uint8_t)su;
         }
+        float sig[VE], rest[VE];
+        sigmoid<false>(g, sig, rest);
 #pragma unroll
-        for (int i = 0; i < VE; i++) h[i] = w * (g[i] * sigmoid(g[i]) * u[i]);
+        for (int i = 0; i < VE; i++) h[i] = w * (g[i] * sig[i] * u[i]);
         if (h_out) st_h<HNT>(h_out + r * I + c, h);
         if (codes) {
 #pragma unroll
@@ -207,13 +237,16 @@ __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt_bwd(const T *__restrict_
 #pragma unroll
             for (int i = 0; i < VE; i++) d[i] = g[i] = u[i] = 0.0f;
         }
+        float s[VE], rest[VE];
+        sigmoid<true>(g, s, rest);
 #pragma unroll
         for (int i = 0; i < VE; i++) {
-            const float s = sigmoid(g[i]), a = g[i] * s, da = w * d[i], au = a * u[i];
+            const float a = g[i] * s[i], da = w * d[i], au = a * u[i];
             dw += d[i] * au;
             h[i] = w * au;
             du[i] = da * a;
-            dg[i] = da * u[i] * (s + a * (1.0f - s));
+            // bf16: 1 - s cancels far below its rounding, and rest costs registers that spill
+            dg[i] = da * u[i] * (s[i] + a * (VE == 4 ? rest[i] : 1.0f - s[i]));
         }
         st_nt(dh13 + at, dg);
         st_nt(dh13 + at + I, du);
