@@ -13,7 +13,21 @@
 
 namespace bsp {
 
-constexpr float kLog2e = 1.44269504088896341f;
+// exp(x) for x <= 0, within 3 + 0.05 |x| units of 2^-24: 2^t (1 + d), t = x log2(e)
+// and d what its rounding left out; without d the error grows with |x| (63 units
+// at 80).  The factor for t is 2^-22 above log2(e), so that d >= 0 and an
+// instruction's clamp to [0, 1] leaves it alone but makes the NaN of x = -inf a 0.
+// V_EXP_F32 flushes results below 2^-126, from x < -87.3, to 0.  NaN stays NaN.
+// Choice and placing of 100003 x 96 take 23.0 us instead of 22.5 for it.
+template <bool FULL = true>
+__device__ __forceinline__ float exp_f32(float x) {
+    constexpr float L2E = 1.44269504088896341f * (1.0f + 0x1p-22f), LN2 = 0.693147180559945309f;
+    if (!FULL) return __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
+    const float t = x * L2E, e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, __builtin_amdgcn_fmed3f(fmaf(-t, LN2, x), 0.0f, 1.0f), e);
+}
+template <bool FULL>
+__device__ __forceinline__ float recip(float x) { return FULL ? 1.0f / x : __builtin_amdgcn_rcpf(x); }
 // From here on fewer lanes to a token pay: choice of 16384 f32 tokens 5.6 us
 // instead of 6.7 for 64 experts and 9.4 instead of 10.2 for 256 (the same for
 // 128), 24000 tokens 6.2 / 8.6 and 10.1 / 12.2; below, 4096 x 128 6.4 instead of 5.1.
@@ -147,12 +161,12 @@ __device__ __forceinline__ void store_logits(T *row, int lane, int E, const floa
 // Softmax of a token whose largest logit is known: v becomes exp(v - m), 0 for
 // -inf; returns the sum over the token.  It is 0 where no logit is above -inf
 // and NaN where one is NaN or +inf.
-template <int L, int V>
+template <int L, bool FULL, int V>
 __device__ __forceinline__ float exp_sum(float (&v)[V], float m) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; i++) {
-        v[i] = __builtin_amdgcn_exp2f((v[i] - m) * kLog2e);
+        v[i] = exp_f32<FULL>(v[i] - m);
         s += v[i];
     }
     return group_sum<L>(s);
@@ -310,7 +324,7 @@ __device__ __forceinline__ void route_select(const RouteArgs &a, int64_t t0, int
         double top[N];
         top_keys<T, L, V, N>(v, lane, top);
         const float best = key_logit(top[0]), m = best > -INFINITY ? best : 0.0f;
-        const float sum = exp_sum<L>(v, m), inv = __builtin_amdgcn_rcpf(sum);   // sum >= 1 where routed
+        const float sum = exp_sum<L, true>(v, m), inv = 1.0f / sum;   // sum >= 1 where routed
         const bool routed = sum > 0.0f, bad = sum != sum;
         if (aux && sum != 0.0f) {             // NaN in a bad row reaches prob_sum and loss
 #pragma unroll
@@ -327,11 +341,11 @@ __device__ __forceinline__ void route_select(const RouteArgs &a, int64_t t0, int
             const float x = key_logit(mine);
             const bool ok = q * L + lane < a.k && routed && x > -INFINITY;
             sel[q] = ok ? key_expert(mine) : -1;
-            val[q] = ok ? __builtin_amdgcn_exp2f((x - m) * kLog2e) : 0.0f;
+            val[q] = ok ? exp_f32(x - m) : 0.0f;
             total += val[q];
         }
         total = group_sum<L>(total);
-        const float scale = bad ? sum : !routed ? 0.0f : a.norm ? __builtin_amdgcn_rcpf(total) : inv;
+        const float scale = bad ? sum : !routed ? 0.0f : a.norm ? 1.0f / total : inv;
 #pragma unroll
         for (int q = 0; q < KS; q++) {
             const int j = q * L + lane;
@@ -1007,6 +1021,7 @@ struct RouteBwdArgs {
 template <typename T, int L, int V, bool VEC>
 __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
     constexpr int KS = 32 / L;                // choices per lane, k <= 32
+    constexpr bool kFull = sizeof(T) == 4;    // a bf16 gradient's rounding hides the difference
     const int tid = threadIdx.x, lane = tid & (L - 1), grp = tid / L;
     const int32_t n = a.counts[a.G];
     const float rn = 1.0f / (n > 0 ? (float)n : 1.0f);
@@ -1051,13 +1066,13 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
         for (int i = 1; i < V; i++) m = fmaxf(m, v[i]);
         m = group_max<L>(m);
         m = m > -INFINITY ? m : 0.0f;
-        const float sum = exp_sum<L>(v, m), inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
+        const float sum = exp_sum<L, kFull>(v, m), inv = sum == 0.0f ? 0.0f : recip<kFull>(sum);
         float dot = 0.0f, ps = 0.0f, pd = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; i++) dot = fmaf(v[i], f[i], dot);
 #pragma unroll
         for (int q = 0; q < KS; q++) {
-            x[q] = __builtin_amdgcn_exp2f((x[q] - m) * kLog2e);
+            x[q] = exp_f32<kFull>(x[q] - m);
             ps += x[q];
             pd = fmaf(x[q], dw[q], pd);
         }
@@ -1065,7 +1080,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
         ps = group_sum<L>(ps);
         pd = group_sum<L>(pd);
         // renormalised: chosen p / ps; else p itself, whose sum of p dw every expert feels
-        const float scale = a.norm ? (ps > 0.0f ? __builtin_amdgcn_rcpf(ps) : 0.0f) : inv;
+        const float scale = a.norm ? (ps > 0.0f ? recip<kFull>(ps) : 0.0f) : inv;
         const float c1 = coef * inv, c2 = c1 * dot + (a.norm ? 0.0f : inv * inv * pd);
 #pragma unroll
         for (int i = 0; i < V; i++) v[i] *= fmaf(c1, f[i], -c2);
