@@ -45,8 +45,8 @@ constexpr int kFewGroups = kMaxGroups / 2;   // placing: groups of the smaller r
 constexpr int kSums = 8, kMaxSlice = 1024 / 4 / kSums;   // workgroups that sum the probabilities, their quads of experts
 
 // Lane exchanges within a row of 16 by DPP.  A token's L lanes (4, 8, 16 or 32)
-// reduce over mirror(16), mirror(8), xor 2, xor 1, each step joining two
-// disjoint sets of lanes; L = 32 starts with the other row of 16.
+// reduce over xor 1, xor 2, mirror(8), mirror(16), each step joining two
+// disjoint sets of lanes; L = 32 ends with the other row of 16.
 enum { DPP_XOR1 = 0xB1, DPP_XOR2 = 0x4E, DPP_MIRROR16 = 0x140, DPP_MIRROR8 = 0x141, DPP_ROR4 = 0x124, DPP_ROR8 = 0x128 };
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
@@ -65,11 +65,25 @@ __device__ __forceinline__ float group_max(float v) {
 }
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
-    if (L == 32) v += __shfl_xor(v, 16, 64);
-    if (L >= 16) v += dpp<DPP_MIRROR16>(v);
-    if (L >= 8) v += dpp<DPP_MIRROR8>(v);
+    v += dpp<DPP_XOR1>(v);
     v += dpp<DPP_XOR2>(v);
-    return v + dpp<DPP_XOR1>(v);
+    if (L >= 8) v += dpp<DPP_MIRROR8>(v);
+    if (L >= 16) v += dpp<DPP_MIRROR16>(v);
+    if (L == 32) v += __shfl_xor(v, 16, 64);
+    return v;
+}
+// The order of a token's sums is that of 8 lanes for up to 128 logits and of 16
+// for more, also on half as many lanes, which long batches use: a lane then holds
+// two lanes' parts, of the even and of the odd pieces, and adds their sums as the
+// last step would have.  A token's weights and gradient do not depend, to the
+// bit, on the size of its batch.
+template <int L, int V>
+constexpr int kParts = (L * V <= 128 ? 8 : 16) == 2 * L ? 2 : 1;
+template <int L, int P>
+__device__ __forceinline__ float parts_sum(const float (&s)[P]) {
+    float v = group_sum<L>(s[0]);
+    if constexpr (P == 2) v += group_sum<L>(s[1]);
+    return v;
 }
 
 // A token's logits on its L lanes, V to a lane in 16-byte pieces of Q values:
@@ -161,15 +175,16 @@ __device__ __forceinline__ void store_logits(T *row, int lane, int E, const floa
 // Softmax of a token whose largest logit is known: v becomes exp(v - m), 0 for
 // -inf; returns the sum over the token.  It is 0 where no logit is above -inf
 // and NaN where one is NaN or +inf.
-template <int L, bool FULL, int V>
+template <typename T, int L, bool FULL, int V>
 __device__ __forceinline__ float exp_sum(float (&v)[V], float m) {
-    float s = 0.0f;
+    constexpr int P = kParts<L, V>;
+    float s[P] = {};
 #pragma unroll
     for (int i = 0; i < V; i++) {
         v[i] = exp_f32<FULL>(v[i] - m);
-        s += v[i];
+        s[i / kPiece<T> % P] += v[i];
     }
-    return group_sum<L>(s);
+    return parts_sum<L, P>(s);
 }
 
 // ---------------------------------------------------------------------------
@@ -308,6 +323,7 @@ constexpr int kSumRows = BT / (L < 16 ? 16 : L);
 template <typename T, int L, int V, int N, int BT, bool VEC>
 __device__ __forceinline__ void route_select(const RouteArgs &a, int64_t t0, int64_t t1, int32_t *hist, float *psum) {
     constexpr int KS = N / L > 0 ? N / L : 1;   // choices a lane writes
+    constexpr int P = kParts<L, V> < KS ? kParts<L, V> : KS;
     const int tid = threadIdx.x, lane = tid & (L - 1), grp = tid / L;
     const bool aux = a.prob_sum != nullptr;
     for (int i = tid; i <= a.G; i += BT) hist[i] = 0;
@@ -324,14 +340,14 @@ __device__ __forceinline__ void route_select(const RouteArgs &a, int64_t t0, int
         double top[N];
         top_keys<T, L, V, N>(v, lane, top);
         const float best = key_logit(top[0]), m = best > -INFINITY ? best : 0.0f;
-        const float sum = exp_sum<L, true>(v, m), inv = 1.0f / sum;   // sum >= 1 where routed
+        const float sum = exp_sum<T, L, true>(v, m), inv = 1.0f / sum;   // sum >= 1 where routed
         const bool routed = sum > 0.0f, bad = sum != sum;
         if (aux && sum != 0.0f) {             // NaN in a bad row reaches prob_sum and loss
 #pragma unroll
             for (int i = 0; i < V; i++) acc[i] = fmaf(v[i], inv, acc[i]);
         }
         int sel[KS];
-        float val[KS], total = 0.0f;
+        float val[KS], part[P] = {};
 #pragma unroll
         for (int q = 0; q < KS; q++) {        // choice j = q L + lane
             double mine = top[q * L];
@@ -342,9 +358,9 @@ __device__ __forceinline__ void route_select(const RouteArgs &a, int64_t t0, int
             const bool ok = q * L + lane < a.k && routed && x > -INFINITY;
             sel[q] = ok ? key_expert(mine) : -1;
             val[q] = ok ? exp_f32(x - m) : 0.0f;
-            total += val[q];
+            part[q % P] += val[q];
         }
-        total = group_sum<L>(total);
+        const float total = parts_sum<L, P>(part);
         const float scale = bad ? sum : !routed ? 0.0f : a.norm ? 1.0f / total : inv;
 #pragma unroll
         for (int q = 0; q < KS; q++) {
@@ -1021,6 +1037,7 @@ struct RouteBwdArgs {
 template <typename T, int L, int V, bool VEC>
 __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
     constexpr int KS = 32 / L;                // choices per lane, k <= 32
+    constexpr int P = kParts<L, V>;
     constexpr bool kFull = sizeof(T) == 4;    // a bf16 gradient's rounding hides the difference
     const int tid = threadIdx.x, lane = tid & (L - 1), grp = tid / L;
     const int32_t n = a.counts[a.G];
@@ -1066,19 +1083,17 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdArgs a) {
         for (int i = 1; i < V; i++) m = fmaxf(m, v[i]);
         m = group_max<L>(m);
         m = m > -INFINITY ? m : 0.0f;
-        const float sum = exp_sum<L, kFull>(v, m), inv = sum == 0.0f ? 0.0f : recip<kFull>(sum);
-        float dot = 0.0f, ps = 0.0f, pd = 0.0f;
+        const float sum = exp_sum<T, L, kFull>(v, m), inv = sum == 0.0f ? 0.0f : recip<kFull>(sum);
+        float dots[P] = {}, sums[P] = {}, grads[P] = {};
 #pragma unroll
-        for (int i = 0; i < V; i++) dot = fmaf(v[i], f[i], dot);
+        for (int i = 0; i < V; i++) dots[i / kPiece<T> % P] = fmaf(v[i], f[i], dots[i / kPiece<T> % P]);
 #pragma unroll
         for (int q = 0; q < KS; q++) {
             x[q] = exp_f32<kFull>(x[q] - m);
-            ps += x[q];
-            pd = fmaf(x[q], dw[q], pd);
+            sums[q % P] += x[q];
+            grads[q % P] = fmaf(x[q], dw[q], grads[q % P]);
         }
-        dot = group_sum<L>(dot) * inv;
-        ps = group_sum<L>(ps);
-        pd = group_sum<L>(pd);
+        const float dot = parts_sum<L, P>(dots) * inv, ps = parts_sum<L, P>(sums), pd = parts_sum<L, P>(grads);
         // renormalised: chosen p / ps; else p itself, whose sum of p dw every expert feels
         const float scale = a.norm ? (ps > 0.0f ? recip<kFull>(ps) : 0.0f) : inv;
         const float c1 = coef * inv, c2 = c1 * dot + (a.norm ? 0.0f : inv * inv * pd);

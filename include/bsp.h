@@ -476,7 +476,8 @@ bsp_status bsp_swiglu_quantize(const void *h13, int in_dtype, int64_t R, int64_t
  * group_offsets and src are the grouped GEMMs' and quantizers' row map with
  * M = T kk; with padding tokens group_offsets[G] < M, and those calls leave
  * the rows of C past it untouched.  Sums are f32 in a fixed order: results
- * are the same on every run.  A row with NaN or +inf logits is not routed; its
+ * are the same on every run, and a token's experts and weights the same, bit
+ * for bit, in every batch and with every row stride.  A row with NaN or +inf logits is not routed; its
  * k weights, prob_sum and loss become NaN.
  *
  * bsp_moe_route_backward: the gradient to the logits of
@@ -492,7 +493,8 @@ bsp_status bsp_swiglu_quantize(const void *h13, int in_dtype, int64_t R, int64_t
  *   d_loss   device f32 [1] or NULL (not both NULL)
  *   d_logits device [T, ldd >= E] of dtype (out); rows of tokens that are not
  *            routed are zeros
- * The probabilities are recomputed from the logits.
+ * The probabilities are recomputed from the logits.  A token's row depends on
+ * the batch through the counts only.
  */
 bsp_status bsp_moe_route(const void *logits, int dtype, int64_t T, int64_t E, int64_t ldl, const uint8_t *token_mask,
                          int64_t k, int64_t shared, int32_t *experts, float *weights, int32_t *counts,
