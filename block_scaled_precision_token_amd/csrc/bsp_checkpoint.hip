@@ -24,6 +24,9 @@
 // h cached 76 (6.6 TB/s); 36864 x 2048 (h 144 MiB): 138, 130, 135.
 // Keeping more than one piece per lane in flight changed nothing for bf16 and
 // cost f32 3 to 10 %.
+// Rows from n_rows on are not loaded: with 20000 of 65536 x 768 unused the
+// forward takes 57.6 us instead of 61.3 and the backward 67.6 instead of 75.7;
+// with all in use the condition costs 0.5 %.
 #include <type_traits>
 
 #include "bsp_moe.hpp"
@@ -178,9 +181,10 @@ __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt(const T *__restrict__ h1
     const T *gp = h13 + r * 2 * I;
     for (int64_t c = lane * VE; c < I; c += LPR * VE) {
         float g[VE], u[VE], h[VE];
-        ld(gp + c, g);
-        ld(gp + I + c, u);
-        if (!used) {
+        if (used) {
+            ld(gp + c, g);
+            ld(gp + I + c, u);
+        } else {
 #pragma unroll
             for (int i = 0; i < VE; i++) g[i] = u[i] = 0.0f;
         }
@@ -227,13 +231,14 @@ __global__ __launch_bounds__(256, 8) void k_swiglu_ckpt_bwd(const T *__restrict_
     for (int64_t c = lane * VE; c < I; c += LPR * VE) {
         const int64_t at = r * 2 * I + c;
         float d[VE], g[VE], u[VE], dg[VE], du[VE], h[VE];
-        Codes<VE> qg, qu;
-        ld(dh + r * I + c, d);
-        ld_codes(ckpt_codes + at, qg);
-        ld_codes(ckpt_codes + at + I, qu);
-        mx_values<VE>(qg, ckpt_scales[at / 32], g);
-        mx_values<VE>(qu, ckpt_scales[(at + I) / 32], u);
-        if (!used) {
+        if (used) {
+            Codes<VE> qg, qu;
+            ld(dh + r * I + c, d);
+            ld_codes(ckpt_codes + at, qg);
+            ld_codes(ckpt_codes + at + I, qu);
+            mx_values<VE>(qg, ckpt_scales[at / 32], g);
+            mx_values<VE>(qu, ckpt_scales[(at + I) / 32], u);
+        } else {
 #pragma unroll
             for (int i = 0; i < VE; i++) d[i] = g[i] = u[i] = 0.0f;
         }
