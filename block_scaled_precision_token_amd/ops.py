@@ -691,7 +691,8 @@ def moe_route(logits: torch.Tensor, k: int, norm: bool = True, shared: int = 0, 
     'prob_sum' f32 [E] and 'loss' f32 [1].
 
     group_offsets and src are the grouped GEMMs' and quantizers' row map (M = T kk).  token_mask (u8 or bool [T])
-    leaves padding tokens out: their experts, src and pos are -1.  See bsp_moe_route in include/bsp.h.
+    leaves padding tokens out: their experts, src and pos are -1.  Like every tensor here it starts on 16 bytes: a part
+    of a longer mask that does not is refused (clone it).  See bsp_moe_route in include/bsp.h.
     """
     dt = _matrix_arg(logits, "logits")
     T, E = logits.shape
@@ -735,7 +736,8 @@ def moe_route_backward(logits: torch.Tensor, k: int, experts, counts, pos, d_wei
                        norm: bool = True, shared: int = 0, token_mask=None, out=None):
     """Gradient [T, E] (logits' dtype) of d_loss * loss + sum(d_weights * row_weights) to the logits, from the
     forward call's experts, counts and pos.  d_weights f32 [T kk] is in grouped-row order, as
-    swiglu_checkpoint_backward returns it; d_loss is a device f32 scalar [1].  See bsp_moe_route_backward."""
+    swiglu_checkpoint_backward returns it; d_loss is a device f32 scalar [1].  Rows of tokens with NaN or +inf logits
+    are NaN, those of padding tokens zeros.  See bsp_moe_route_backward."""
     dt = _matrix_arg(logits, "logits")
     T, E = logits.shape
     dev = logits.device

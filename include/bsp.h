@@ -42,7 +42,8 @@
  *     [rows, K/16], MXFP8 E8M0 [rows, K/32].
  *   - Device pointers must be 16-byte aligned.  Arguments are validated on
  *     the host before anything is launched; an invalid call returns an error
- *     and enqueues nothing.  Inputs must be finite.
+ *     and enqueues nothing.  Inputs must be finite, except where a
+ *     call says what becomes of others.
  *   - Bit-exactness: codes and scales are a pure function of the inputs
  *     (IEEE f32 arithmetic, no fast math), identical to the reference
  *     definition for every launch geometry.
@@ -477,8 +478,8 @@ bsp_status bsp_swiglu_quantize(const void *h13, int in_dtype, int64_t R, int64_t
  * M = T kk; with padding tokens group_offsets[G] < M, and those calls leave
  * the rows of C past it untouched.  Sums are f32 in a fixed order: results
  * are the same on every run, and a token's experts and weights the same, bit
- * for bit, in every batch and with every row stride.  A row with NaN or +inf logits is not routed; its
- * k weights, prob_sum and loss become NaN.
+ * for bit, in every batch and with every row stride.  A row with NaN or +inf
+ * logits (mask not 0) is not routed; its k weights, prob_sum and loss become NaN.
  *
  * bsp_moe_route_backward: the gradient to the logits of
  *   d_loss * loss + sum_{t, j < k} d_weights[pos[t, j]] * weights[t, j]
@@ -491,8 +492,9 @@ bsp_status bsp_swiglu_quantize(const void *h13, int in_dtype, int64_t R, int64_t
  *            bsp_swiglu_checkpoint_backward writes d_row_weights) or NULL;
  *            entries of shared groups are ignored
  *   d_loss   device f32 [1] or NULL (not both NULL)
- *   d_logits device [T, ldd >= E] of dtype (out); rows of tokens that are not
- *            routed are zeros
+ *   d_logits device [T, ldd >= E] of dtype (out); zeros for tokens whose mask
+ *            is 0 or whose logits are all -inf; NaN for other tokens with a NaN
+ *            or +inf logit
  * The probabilities are recomputed from the logits.  A token's row depends on
  * the batch through the counts only.
  */
@@ -552,7 +554,7 @@ bsp_status bsp_swiglu_checkpoint_backward(const void *dh, int dtype, int64_t R, 
  *   out[t, :] = sum_j weights[t, j] * y[pos[t, j], :]   (f32, in order of j)
  *   y        device [rows, ldy >= H] of in_dtype (f32 or bf16)
  *   pos      device int32 [T, kk], 1 <= kk <= 128; an index outside [0, rows)
- *            contributes nothing (and nothing is read for it)
+ *            contributes nothing, whatever the rows of y hold
  *   weights  device f32 [T, kk] or NULL (all 1)
  *   out      device [T, ldo >= H] of out_dtype (f32 or bf16)
  *   H, ldy, ldo multiples of 8
