@@ -859,8 +859,10 @@ __device__ __forceinline__ void route_sums(const RouteArgs &a, int i, int32_t *t
 // words for each of G + 1 columns from L2, which is less than a third launch
 // costs.  Bound by the latency of its phases: 8192 x 128 5.8 us, 8192 x 512 6.6,
 // 100003 x 96 8.6, of which the histograms' round trip and sums are about 2.
+template <int NT, int W, int GROUPS>   // wavefronts per SIMD: the largest table leaves room for one workgroup of 512
+constexpr int kPlaceWaves = NT == 512 && W == 8 && GROUPS == kMaxGroups ? 2 : 4;
 template <typename HT, int NT, int W, int GROUPS>
-__global__ __launch_bounds__(NT, 4) void k_route_place(RouteArgs a) {
+__global__ __launch_bounds__(NT, (kPlaceWaves<NT, W, GROUPS>)) void k_route_place(RouteArgs a) {
     constexpr int H = 4;
     __shared__ int32_t tot[GROUPS + 1], before[GROUPS + 1], base[GROUPS];
     __shared__ PlaceTable<H, NT, W, GROUPS> tab;
