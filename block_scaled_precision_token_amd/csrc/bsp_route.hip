@@ -28,12 +28,12 @@ __device__ __forceinline__ float exp_f32(float x) {
 }
 template <bool FULL>
 __device__ __forceinline__ float recip(float x) { return FULL ? 1.0f / x : __builtin_amdgcn_rcpf(x); }
-// From here on fewer lanes to a token pay: choice of 16384 f32 tokens 5.6 us
-// instead of 6.7 for 64 experts and 9.4 instead of 10.2 for 256 (the same for
-// 128), 24000 tokens 6.2 / 8.6 and 10.1 / 12.2; below, 4096 x 128 6.4 instead of 5.1.
+// From about here on fewer lanes to a token pay: choice of 16384 f32 tokens 5.9 us
+// (with more lanes 6.0) for 64 experts, 7.4 (6.7) for 128 and 10.5 (10.9) for 256,
+// 24000 x 256 11.9 (14.0), 131072 x 256 34.8 (52.1); below, 4096 x 128 6.8 (5.3).
 constexpr int64_t kManyTokens = 16384;
 // Gradient: three workgroups to a compute unit, as the registers of the widest
-// form allow (65537 x 256 bf16: 19.7 us, with 1536 22.8).
+// form allow (65537 x 256 bf16: 19.9 us, with 1536 23.4).
 constexpr int64_t kBwdWorkgroups = 768;
 // Batches that one workgroup finishes in one launch: of 256 threads, or of 1024
 // for up to 256 experts and k <= 8 (128 tokens, 128 experts: 10.5 us a call
@@ -674,8 +674,8 @@ __device__ __forceinline__ int32_t lanes_sum(int32_t v) {
     return v + __builtin_amdgcn_mov_dpp(v, DPP_XOR1, 0xF, 0xF, true);
 }
 
-// First launch, bound by the vector units (8192 x 128 5.4 us, 100003 x 96 14.4 us,
-// of which 7.9 are the issue of its vector instructions).  A batch of one run of at most ONE tokens is finished here, by
+// First launch, bound by the vector units (8192 x 128 5.6 us, 100003 x 96 15.4 us,
+// of which 8.7 are the issue of its vector instructions).  A batch of one run of at most ONE tokens is finished here, by
 // its one workgroup (ONE = 0: there are more runs).
 template <typename T, int L, int V, int N, int BT, int ONE, bool VEC>
 __global__ __launch_bounds__(BT) void k_route_select(RouteArgs a) {
@@ -910,7 +910,8 @@ int64_t route_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t shared) {
 
 template <typename T, int L, int V, int N, bool VEC>
 static void route_launch_few(const RouteArgs &a, hipStream_t s) {
-    // threads: 8192 x 512 13.2 us with 256, 10.9 with 512; the longer lists need the registers
+    // threads: 8192 x 512 12.0 us with 256, 11.1 with 512, 65536 x 512 52.0 and 42.7 (8192 x 128, whose runs
+    // fill 256, 5.4 and 5.6); the longer lists need the registers
     constexpr int B = N == 8 ? 512 : 256;
     if (a.T <= kOneSmallTokens) {
         k_route_select<T, L, V, N, 256, kOneSmallTokens, VEC><<<1, 256, 0, s>>>(a);
@@ -927,10 +928,10 @@ static void route_few(const RouteArgs &a, hipStream_t s) {
     else if (a.k <= 16) route_launch_few<T, L, V, 16, VEC>(a, s);
     else route_launch_few<T, L, V, 32, VEC>(a, s);
 }
-// Lanes and logits to a lane, f32, choice of 8192 tokens: 64 experts 4.7 us with
-// 8 x 8 and 5.2 with 16 x 4; 128: 5.2 with 8 x 16, 5.6 with 16 x 8; 256: 6.7 with
-// 16 x 16, 8.3 with 32 x 8; 512: 10.0 with 16 x 32, 10.9 with 32 x 16 (65536
-// tokens: 36.8 and 51.4).
+// Lanes and logits to a lane, f32, choice of 8192 tokens: 64 experts 4.9 us with
+// 8 x 8 and 5.6 with 16 x 4; 128: 5.6 with 8 x 16, 6.0 with 16 x 8; 256: 7.1 with
+// 16 x 16, 9.0 with 32 x 8; 512: 11.1 with 16 x 32, 11.9 with 32 x 16 (65536
+// tokens: 42.7 and 59.6).
 template <typename T, bool VEC>
 static void route_few_experts(const RouteArgs &a, hipStream_t s) {
     if (a.E <= 64) route_few<T, 8, 8, VEC>(a, s);
@@ -943,9 +944,9 @@ static void route_few_experts(const RouteArgs &a, hipStream_t s) {
 // Many tokens: four or eight lanes to a token, with as many logits each as the
 // experts need (in eights), so that a wavefront's instructions cover 16 or 8
 // tokens and the lists cross two or three steps between lanes.  Measured at
-// 100003 x 96: choice 14.2 us with 4 lanes of 24 logits, 17.7 with 4 of 32, 18.8
-// with 8 of 16 and 27.6 with 16 of 8; at 8192 x 128, where the wavefronts are
-// too few to fill the GPU, 8 lanes take 5.4 us and 4 lanes 8.2.
+// 100003 x 96: choice 15.4 us with 4 lanes of 24 logits, 18.4 with 4 of 32, 20.9
+// with 8 of 16 and 29.7 with 16 of 8; at 8192 x 128, where the wavefronts are
+// too few to fill the GPU, 8 lanes take 5.6 us and 4 lanes 7.1.
 constexpr int kManyThreads = 768;
 template <typename T, int L, int V>
 static void route_many(const RouteArgs &a, hipStream_t s) {
@@ -1028,8 +1029,8 @@ struct RouteBwdArgs {
     const float *d_weights, *d_loss;
 };
 
-// Bound by HBM, every logit read and written once (8192 x 128 f32 4.8 us; 65537 x
-// 256 bf16 19.7 us, 3.8 TB/s): a wavefront's loads of a token's logits and choices
+// Bound by HBM, every logit read and written once (8192 x 128 f32 4.9 us; 65537 x
+// 256 bf16 19.9 us, 3.7 TB/s): a wavefront's loads of a token's logits and choices
 // go out together, then the gathers by the choice, and loading the next token's
 // ahead of them gained nothing.  Per element the terms that every expert has are
 // one multiply-add of the count and one product, e (c1 f - c2); the k chosen
@@ -1119,11 +1120,11 @@ static void route_bwd_launch(const RouteBwdArgs &a, hipStream_t s) {
     const unsigned grid = (unsigned)(wgs < kBwdWorkgroups ? wgs : kBwdWorkgroups);
     k_route_bwd<T, L, V, VEC><<<grid, 256, 0, s>>>(a);
 }
-// Lanes and logits to a lane: 128 experts 8 x 16 (65536 tokens f32: 16.1 us, 16 x 8
-// 17.3, 4 x 32 19.3; 32768 bf16: 9.0, 10.4, 9.5); 256 experts 16 x 16, in bf16 and
-// with many tokens 8 x 32 (65537 bf16: 19.7 instead of 21.4; but 20000 f32 12.8
-// instead of 11.8, and 4096 f32 5.4 instead of 5.0); 512 experts 32 x 16 (65536
-// f32: 53.8, 16 x 32 58.2).
+// Lanes and logits to a lane: 128 experts 8 x 16 (65536 tokens f32: 16.2 us, 16 x 8
+// 18.0, 4 x 32 19.9; 32768 bf16: 9.1, 10.6, 9.5); 256 experts 16 x 16, in bf16 and
+// with many tokens 8 x 32 (65537 bf16: 19.9 instead of 21.4; but 20000 f32 12.7
+// instead of 12.2, and 4096 f32 5.7 instead of 5.1); 512 experts 32 x 16 (65536
+// f32: 54.0, 16 x 32 58.6).
 template <typename T, bool VEC>
 static void route_bwd_dispatch(const RouteBwdArgs &a, hipStream_t s) {
     constexpr int Q = kPiece<T>;
