@@ -2,13 +2,20 @@
 // values share one power-of-two scale): MXFP4 x MXFP4, MXFP8 x MXFP4 and, for
 // the gated block, MXFP8 x MXFP8; and the gated feed-forward block on them.
 //
-// gfx950's block-scaled matrix instruction V_MFMA_SCALE_F32_32X32X64_F8F6F4
-// takes codes and E8M0 scales as they are stored.  Lane l supplies row l % 32
-// of its operand: in MXFP4 the 32 values of K block l / 32 (16 bytes), in
-// MXFP8 16 values of each of the two K blocks (16 bytes at 16 (l / 32) of
-// each), with the scale of block l / 32.  MXFP4 products are exact in its sum
-// up to f32's own rounding (0 to 1e-7 of the result measured), MXFP8 ones
-// carry an error of about 5e-6 (x MXFP4) or 1.5e-5 (x MXFP8) of it.
+// MXFP4 x MXFP4: gfx950's block-scaled matrix instruction
+// V_MFMA_SCALE_F32_32X32X64_F8F6F4 takes codes and E8M0 scales as they are
+// stored.  Lane l supplies row l % 32 of its operand, the 32 values of K block
+// l / 32 (16 bytes) and that block's scale.  Its sums of MXFP4 products carry
+// f32's own rounding alone.
+// MXFP8 tokens: that instruction would drop what lies far below its largest
+// product (64 values with blocks 2^5 apart: up to 1e-4 of sum |a b|), so their
+// products are V_MFMA_F32_32X32X16_BF16's, on values times scales, which bf16
+// holds exactly (to_bf16): a row's sums are the same to f32's rounding whatever
+// form its batch takes.  At a quarter of the MXFP4 rate, near what the card's
+// power sustains in bf16 (8192^3 by the library 1203 TFLOP/s), they bound large
+// calls: the gated block of 8192 tokens takes 468 us, 297 by the scaled
+// instruction.  The lanes hold the same 32-value block of both operands here too
+// and multiply it eight values at a time.
 //
 // The weights are the instruction's first operand and the tokens the second,
 // so a lane ends with one token and 16 of 32 consecutive columns of C (lane
@@ -58,10 +65,34 @@ struct IC {
     static constexpr int v = V;
 };
 
-// acc += N block x T block of one 64-value step; the scales are byte ON of sn and byte OT of st.
-template <int FT, int FN, int ON, int OT>
+// acc += N block x T block of one 64-value step, both MXFP4; the scales are byte ON of sn and byte OT of st.
+template <int ON, int OT>
 __device__ __forceinline__ v16f mma(v8i n, v8i t, v16f acc, int sn, int st) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(n, t, acc, FN == 4 ? 4 : 0, FT == 4 ? 4 : 0, ON, sn, OT, st);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(n, t, acc, 4, 4, ON, sn, OT, st);
+}
+
+// Values 8 q .. 8 q + 7 of a lane's block times its scale (byte `at` of `scale`) in bf16, exactly down to 2^-133, for
+// scale codes up to 246 (MXFP8) and 252 (MXFP4), the quantizers' largest.
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+template <int F>
+__device__ __forceinline__ v8bf to_bf16(v8i c, int q, uint32_t scale, int at) {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    const float s = __uint_as_float(((scale >> (8 * at)) & 255u) << 23);   // the exponent alone counts; 0 is 2^-127
+    v2bf r[4];
+    if constexpr (F == 4) {
+        const uint32_t x = (uint32_t)c[q];
+        r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 0);
+        r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 1);
+        r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 2);
+        r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 3);
+    } else {
+        const uint32_t x = (uint32_t)c[2 * q], y = (uint32_t)c[2 * q + 1];
+        r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, false);
+        r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, true);
+        r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y, s, false);
+        r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y, s, true);
+    }
+    return v8bf{r[0][0], r[0][1], r[1][0], r[1][1], r[2][0], r[2][1], r[3][0], r[3][1]};
 }
 
 // ---------------------------------------------------------------------------
@@ -382,35 +413,7 @@ __device__ __forceinline__ bool find_tile(const int64_t *off, int G, int M, int 
 // A workgroup has 32 tokens and 64 rows of B; its eight wavefronts take every
 // eighth chunk of 256 K values, straight from global memory into registers,
 // and their sums meet in LDS.  The weights are read once and are what bounds
-// this form: a chunk's loads are all issued before its first product.  With
-// MXFP8 tokens the products are bf16's, on the operands' exact values: the
-// scaled instruction's sums lose 5e-6 of the result there, which moves a code of
-// h to its neighbour now and then, and a memory-bound form has the time (the
-// lanes then hold the same 32-value block of both operands).
-// Values 8 q .. 8 q + 7 of a lane's block in bf16, which holds each of them times its scale (byte `at` of `scale`) exactly
-// down to 2^-133.
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-template <int F>
-__device__ __forceinline__ v8bf few_bf16(v8i c, int q, uint32_t scale, int at) {
-    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-    const float s = __uint_as_float(((scale >> (8 * at)) & 255u) << 23);   // the conversions take the exponent alone
-    v2bf r[4];
-    if constexpr (F == 4) {
-        const uint32_t x = (uint32_t)c[q];
-        r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 0);
-        r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 1);
-        r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 2);
-        r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 3);
-    } else {
-        const uint32_t x = (uint32_t)c[2 * q], y = (uint32_t)c[2 * q + 1];
-        r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, false);
-        r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, true);
-        r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y, s, false);
-        r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y, s, true);
-    }
-    return v8bf{r[0][0], r[0][1], r[1][0], r[1][1], r[2][0], r[2][1], r[3][0], r[3][1]};
-}
-
+// this form: a chunk's loads are all issued before its first product.
 template <int FT, int FN, int EPI>
 __global__ __launch_bounds__(512) void k_mx_few(MxArgs p) {
     __shared__ float part[8][32][64];
@@ -495,16 +498,15 @@ __global__ __launch_bounds__(512) void k_mx_few(MxArgs p) {
                 if constexpr (FT == 4) {
 #pragma unroll
                     for (int j = 0; j < 2; j++)
-                        acc[j] = mma<FT, FN, 2 * (s & 1), 2 * (s & 1)>(b[s][j], a[s], acc[j], (int)sn[j][s >> 1],
-                                                                       (int)st[s >> 1]);
+                        acc[j] = mma<2 * (s & 1), 2 * (s & 1)>(b[s][j], a[s], acc[j], (int)sn[j][s >> 1], (int)st[s >> 1]);
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; q++) {
-                        const v8bf t = few_bf16<FT>(a[s], q, st[s >> 1], 2 * (s & 1));
+                        const v8bf t = to_bf16<FT>(a[s], q, st[s >> 1], 2 * (s & 1));
 #pragma unroll
                         for (int j = 0; j < 2; j++)
                             acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                                few_bf16<FN>(b[s][j], q, sn[j][s >> 1], 2 * (s & 1)), t, acc[j], 0, 0, 0);
+                                to_bf16<FN>(b[s][j], q, sn[j][s >> 1], 2 * (s & 1)), t, acc[j], 0, 0, 0);
                     }
                 }
             }
@@ -1040,14 +1042,14 @@ __global__ __launch_bounds__((MxGeo<FT, FN, TB>::NT), 2) void k_mx_tile(MxArgs p
         if constexpr (FT == 4) {
             ft[s][0] = rt * Geo::RT + 16 * ((2 * s + lh) ^ swizzle<CHT>(rt));
         } else {
-            ft[s][0] = rt * Geo::RT + 16 * ((4 * s + lh) ^ swizzle<CHT>(rt));
-            ft[s][1] = rt * Geo::RT + 16 * ((4 * s + 2 + lh) ^ swizzle<CHT>(rt));
+            ft[s][0] = rt * Geo::RT + 16 * ((4 * s + 2 * lh) ^ swizzle<CHT>(rt));
+            ft[s][1] = rt * Geo::RT + 16 * ((4 * s + 2 * lh + 1) ^ swizzle<CHT>(rt));
         }
         if constexpr (FN == 4) {
             fn[s][0] = Geo::CT + rn * Geo::RN + 16 * ((2 * s + lh) ^ swizzle<CHN>(rn));
         } else {
-            fn[s][0] = Geo::CT + rn * Geo::RN + 16 * ((4 * s + lh) ^ swizzle<CHN>(rn));
-            fn[s][1] = Geo::CT + rn * Geo::RN + 16 * ((4 * s + 2 + lh) ^ swizzle<CHN>(rn));
+            fn[s][0] = Geo::CT + rn * Geo::RN + 16 * ((4 * s + 2 * lh) ^ swizzle<CHN>(rn));
+            fn[s][1] = Geo::CT + rn * Geo::RN + 16 * ((4 * s + 2 * lh + 1) ^ swizzle<CHN>(rn));
         }
     }
     const uint32_t st = Geo::ST + ((wt * 32 + lr) * 2 + lh) * Geo::TCH, sn = Geo::SN + ((wn * 32 + lr) * 2 + lh) * Geo::NCH;
@@ -1100,18 +1102,37 @@ __global__ __launch_bounds__((MxGeo<FT, FN, TB>::NT), 2) void k_mx_tile(MxArgs p
             // byte 4 d + o of a chunk is byte o of word d
             constexpr int q = decltype(Q)::v, i = decltype(I)::v, bt = i * U + q;
             constexpr int h = q & (PRE - 1);
-            acc[i][0] = mma<FT, FN, q & 3, bt & 3>(n[h][0], a[h][i], acc[i][0], (int)sb[q >> 2], (int)sa[bt >> 2]);
-            acc[i][1] = mma<FT, FN, (U + q) & 3, bt & 3>(n[h][1], a[h][i], acc[i][1], (int)sb[(U + q) >> 2], (int)sa[bt >> 2]);
+            acc[i][0] = mma<q & 3, bt & 3>(n[h][0], a[h][i], acc[i][0], (int)sb[q >> 2], (int)sa[bt >> 2]);
+            acc[i][1] = mma<(U + q) & 3, bt & 3>(n[h][1], a[h][i], acc[i][1], (int)sb[(U + q) >> 2], (int)sa[bt >> 2]);
+        };
+        // The same in bf16, eight values of each lane's block at a time.
+        auto exact = [&](auto Q) __attribute__((always_inline)) {
+            constexpr int q = decltype(Q)::v;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const v8bf n0 = to_bf16<FN>(n[0][0], e, sb[0], q), n1 = to_bf16<FN>(n[0][1], e, sb[0], U + q);
+#pragma unroll
+                for (int i = 0; i < TI; i++) {
+                    const v8bf x = to_bf16<FT>(a[0][i], e, sa[0], i * U + q);
+                    acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n0, x, acc[i][0], 0, 0, 0);
+                    acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n1, x, acc[i][1], 0, 0, 0);
+                }
+            }
         };
         auto step = [&](auto Q) __attribute__((always_inline)) {
             constexpr int q = decltype(Q)::v;
             if constexpr (q < SUB) {
-                // the next step's fragments (MXFP8 ones take twice the registers and are read when it begins)
+                // the next step's fragments (with MXFP8 tokens the bf16 products bound the step: read when it begins)
                 if constexpr (FT == 4 && q + 1 < SUB) load(q + 1);
                 if constexpr (FT == 8 && q > 0) load(q);
                 issue(Q);
-                two(Q, IC<0>{});
-                if constexpr (TI > 1) two(Q, IC<1>{});
+                if constexpr (FT == 4) {
+                    two(Q, IC<0>{});
+                    if constexpr (TI > 1) two(Q, IC<1>{});
+                } else {
+                    static_assert(FT == 4 || Geo::TCH <= 4, "a lane's scales in one word");
+                    exact(Q);
+                }
                 asm volatile("" ::: "memory");   // no fragments further ahead: they would not fit the registers
             }
         };

@@ -342,7 +342,10 @@ bsp_status bsp_requant_transpose_sr_batched(const uint8_t *codes, const uint8_t 
  * BSP_FMT_MXFP4 takes both operands as bsp_quantize_mxfp4 makes them,
  * BSP_FMT_MXFP8_MXFP4 an MXFP8 A and an MXFP4 B (8-bit activations, 4-bit
  * weights); all modes, no outer scales, WGRAD on the grouped columnwise copies.
- * The matrix core applies the block scales.  Calls of at most BSP_FEW_ROWS rows
+ * Products of values times scales are exact and their sums f32: a call's error
+ * is f32's rounding of the running sums.  Scale codes are the quantizers': at
+ * most 246 (MXFP8) and 252 (MXFP4); with an MXFP8 A, values times scales are
+ * rounded to multiples of 2^-133.  Calls of at most BSP_FEW_ROWS rows
  * (FPROP, DGRAD) take a form for serving that needs no workspace (size 0, NULL
  * accepted).  Sizes: A's codes and one expert's B below 4 GiB.
  *   workspace  device, >= bsp_gemm_workspace_size(fmt, mode, M, N, K, G)
@@ -622,9 +625,8 @@ bsp_status bsp_swiglu_checkpoint_backward(const void *dh, int dtype, int64_t R, 
  *   workspace  device, >= bsp_moe_gated_backward_workspace_size(fmt, R, I, K, G)
  *            bytes (NULL if R <= BSP_FEW_ROWS and d_row_weights is NULL)
  * Rows from group_offsets[G] on are neither read nor written.  Sums are in a fixed
- * order: results repeat bit for bit.  MXFP4 products are exact to f32's rounding,
- * those with MXFP8 operands to about 2^-16 of the result (the matrix core's sums),
- * or to f32's too in calls of at most BSP_FEW_ROWS rows.
+ * order: results repeat bit for bit.  gate, up and dh carry f32's rounding of their
+ * sums, in all formats.
  */
 bsp_status bsp_moe_gated(int fmt, const uint8_t *a_codes, const uint8_t *a_scales, const int32_t *a_gather,
                          int64_t a_rows, const int64_t *group_offsets, int64_t G, int64_t R, int64_t I, int64_t K,
