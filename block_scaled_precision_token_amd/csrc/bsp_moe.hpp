@@ -135,11 +135,11 @@ __device__ __forceinline__ void st8(uint16_t *p, const float (&v)[8]) {
 }
 
 // s = 1 / (1 + e), e = exp(-z), and (FULL) c = 1 - s = e s, of VE values.
-// FULL, for f32 results: e = 2^t (1 + d), t = -z log2(e) rounded and d what the
+// FULL, for f32 results and for codes that are rounded from them: e = 2^t (1 + d), t = -z log2(e) rounded and d what the
 // rounding left out; without d the error of e grows with |z| (2.8 units of 2^-24
 // at 4, 60 at 80).  With it s is within 6 + 0.05 |z| units and c, which 1 - s
-// would cancel, within 10 + 0.1 |z|.  The forward's h is rounded to bf16 and does
-// without.  Past |z| = 87 2^t, the reciprocal (V_RCP_F32 flushes results below
+// would cancel, within 10 + 0.1 |z|.  swiglu_checkpoint's h is rounded to bf16
+// first and does without.  Past |z| = 87 2^t, the reciprocal (V_RCP_F32 flushes results below
 // 2^-126) and d run out of range; a wavefront that has such a value takes exp(z)
 // for s there, scaled by 2^64 until the end: subnormal from -87.3, 0 below -104.
 template <bool FULL, int VE>

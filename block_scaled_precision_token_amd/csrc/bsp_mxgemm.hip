@@ -332,7 +332,7 @@ __device__ __forceinline__ void epilogue(const MxArgs &p, v16f (&acc)[2], int g,
             store_mx(v[1], BSP_FMT_MXFP8, p.ckpt_codes + at + p.I, p.ckpt_scales + (at + p.I) / 32, lh);
         }
         float h[16], s[16], rest[16];
-        sigmoid<false>(v[0], s, rest);
+        sigmoid<true>(v[0], s, rest);   // h is rounded once, to 3 bits or to bf16, from f32
 #pragma unroll
         for (int e = 0; e < 16; e++) h[e] = w * (v[0][e] * s[e] * v[1][e]);
         const int64_t at = (int64_t)r * p.I + col;
@@ -1258,7 +1258,7 @@ __global__ __launch_bounds__((MxGeo<FT, FN, TB>::NT), 2) void k_mx_tile(MxArgs p
                 }
                 {
                     float s[16], rest[16];
-                    sigmoid<false>(v[0], s, rest);
+                    sigmoid<true>(v[0], s, rest);   // h is rounded once, to 3 bits or to bf16, from f32
 #pragma unroll
                     for (int e = 0; e < 16; e++) h[e] = rw * (v[0][e] * s[e] * v[1][e]);
                 }
