@@ -181,7 +181,8 @@ __device__ __forceinline__ float block_max(const float (&v)[16]) {
 }
 // The conversions divide by the block's scale themselves: the same codes as from x * 2^-k for every f32 within the
 // format (checked exhaustively for a dozen exponents).  V_CVT_SCALEF32_PK_FP8_F32 does not saturate: values past
-// 448 * 2^k, as blocks past the largest exponent have, are clamped before it.
+// 448 * 2^k, as blocks past the largest exponent have, are clamped before it.  A NaN becomes the NaN code on either path
+// (V_MED3_F32 would make it -TOP, in whatever wavefronts clamp).
 __device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d, float scale) {
     typedef short s2 __attribute__((ext_vector_type(2)));
     s2 o = {0, 0};
@@ -198,7 +199,7 @@ __device__ __forceinline__ uint32_t mx8_block(const float (&v)[16], u32v4 &codes
     if (__any(top > TOP)) {
         float c[16];
 #pragma unroll
-        for (int e = 0; e < 16; e++) c[e] = __builtin_amdgcn_fmed3f(v[e], -TOP, TOP);
+        for (int e = 0; e < 16; e++) c[e] = v[e] != v[e] ? v[e] : __builtin_amdgcn_fmed3f(v[e], -TOP, TOP);
 #pragma unroll
         for (int q = 0; q < 4; q++) d[q] = fp8x4(c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3], s);
     } else {

@@ -609,7 +609,8 @@ bsp_status bsp_swiglu_checkpoint_backward(const void *dh, int dtype, int64_t R, 
  *            h quantized along I, from its f32 values.  h_out or h_fmt is needed.
  *   ckpt_codes, ckpt_scales  device u8 [R, 2I], [R, 2I/32], or both NULL (out):
  *            gate and up as rowwise MXFP8, from their f32 values: what
- *            bsp_swiglu_checkpoint_backward and the call below take
+ *            bsp_swiglu_checkpoint_backward and the call below take.  In h and
+ *            here a NaN is E4M3's NaN code, infinities are +-448 * 2^119.
  *   workspace  device, >= bsp_moe_gated_workspace_size(fmt, R, I, K, G) bytes,
  *            rewritten by every call; none (NULL) for R <= BSP_FEW_ROWS
  *   tile     0, or 32 / 128 as in bsp_moe_grouped_gemm_blockscaled_tiled
