@@ -138,6 +138,11 @@ __device__ __forceinline__ int mx4_block_exponent(float amax) {
     k = k < -127 ? -127 : k;
     return k > 125 ? 125 : k;
 }
+// The block's scale code: E2M1 has no NaN, so a block with one (amax is NaN, by max_nan) has E8M0's NaN as its scale.
+__device__ __forceinline__ uint32_t mx4_scale(float amax, int k) { return amax != amax ? 255u : (uint32_t)(k + 127); }
+
+// The larger of two values, NaN if one is (V_MAXIMUM3_F32).
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
 // 2^(c - 127) of an E8M0 scale code c <= 254 (2^-127 is a subnormal f32).
 __device__ __forceinline__ float e8m0_value(uint32_t c) { return __uint_as_float(c ? c << 23 : 0x00400000u); }

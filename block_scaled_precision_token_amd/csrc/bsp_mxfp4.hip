@@ -4,6 +4,7 @@
 //
 //   k = smallest integer with amax <= 6 * 2^k (never clips), in [-127, 125]
 //   code = E2M1(x * 2^-k): x * 2^-k is exact in f32 (0 far below the grid), so each value is rounded once
+//   a block with a NaN: scale 255, with which the conversions and the matrix instructions give NaN for any code
 //
 // HBM bounds: 2 bytes in and 17/32 bytes out per value and copy.  8192 x 2048 in
 // both copies takes 15 us (51 MB, 3.4 TB/s), 65536 x 1536 by groups and rounded
@@ -50,7 +51,7 @@ __device__ __forceinline__ void unpack8(uint4 raw, float (&x)[8]) {
 __device__ __forceinline__ float amax8(const float (&x)[8]) {
     float a = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; j++) a = fmaxf(a, fabsf(x[j]));
+    for (int j = 0; j < 8; j++) a = max_nan(a, fabsf(x[j]));
     return a;
 }
 
@@ -59,10 +60,10 @@ template <bool SR>
 __device__ __forceinline__ uint32_t row_codes(const float (&x)[8], uint64_t blk, uint32_t key0, uint32_t key1,
                                               uint32_t &scale) {
     float a = amax8(x);
-    a = fmaxf(a, __shfl_xor(a, 1, 64));
-    a = fmaxf(a, __shfl_xor(a, 2, 64));
+    a = max_nan(a, __shfl_xor(a, 1, 64));
+    a = max_nan(a, __shfl_xor(a, 2, 64));
     const int k = mx4_block_exponent(a);
-    scale = (uint32_t)(k + 127);
+    scale = mx4_scale(a, k);
     const float r = exp2i(-k);
     return SR ? pack8_stochastic(x, r, blk, 0u, key0, key1) : pack8_nearest(x, r);
 }
@@ -212,7 +213,7 @@ __global__ __launch_bounds__(256) void k_mxfp4_tile(const uint16_t *__restrict__
 #pragma unroll
         for (int i = 0; i < 32; i++) f[i >> 3][i & 7] = __uint_as_float((uint32_t)tile[64 * rh + 32 * b + i][c] << 16);
 #pragma unroll
-        for (int i = 0; i < 4; i++) a = fmaxf(a, amax8(f[i]));
+        for (int i = 0; i < 4; i++) a = max_nan(a, amax8(f[i]));
         const int k = mx4_block_exponent(a);
         const float r = exp2i(-k);
         uint32_t w[4];
@@ -221,7 +222,7 @@ __global__ __launch_bounds__(256) void k_mxfp4_tile(const uint16_t *__restrict__
             w[i] = SR ? pack8_stochastic(f[i], r, (colel + (uint64_t)(kcol * ld + pb)) / 8 + i, 1u, key0, key1)
                       : pack8_nearest(f[i], r);
         q[b] = make_uint4(w[0], w[1], w[2], w[3]);
-        if (kcol < K && pb < ptotal) scales_colT[kcol * (ld / 32) + pb / 32] = (uint8_t)(k + 127);
+        if (kcol < K && pb < ptotal) scales_colT[kcol * (ld / 32) + pb / 32] = (uint8_t)mx4_scale(a, k);
     }
     __syncthreads();   // the input tile is no longer read
 
@@ -247,10 +248,10 @@ __global__ __launch_bounds__(256) void k_dequant_mxfp4(const uint8_t *__restrict
     const int64_t i = grid_index() * 256 + threadIdx.x;
     if (i >= n8) return;
     const uint32_t c = reinterpret_cast<const uint32_t *>(codes)[i];
-    const float s = e8m0_value(scales[i / 4]);
-    const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0), v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
-    const auto v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2), v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
-    const float y[8] = {v0[0] * s, v0[1] * s, v1[0] * s, v1[1] * s, v2[0] * s, v2[1] * s, v3[0] * s, v3[1] * s};
+    const float s = __uint_as_float((uint32_t)scales[i / 4] << 23);   // its exponent alone counts: 0 is 2^-127, 255 NaN
+    const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0), v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
+    const auto v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2), v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
+    const float y[8] = {v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
     if (BF16) st8<true>(reinterpret_cast<uint16_t *>(out) + 8 * i, y);
     else st8<true>(reinterpret_cast<float *>(out) + 8 * i, y);
 }

@@ -212,7 +212,13 @@ __device__ __forceinline__ uint32_t mx8_block(const float (&v)[16], u32v4 &codes
     return (uint32_t)(k + 127);
 }
 __device__ __forceinline__ uint32_t mx4_block(const float (&v)[16], uint2 &codes) {
-    const int k = mx4_block_exponent(block_max(v));
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; i++) top = max_nan(top, fabsf(v[i]));
+    uint32_t a = __float_as_uint(top), b = a;
+    swap32(a, b);
+    top = max_nan(__uint_as_float(a), __uint_as_float(b));
+    const int k = mx4_block_exponent(top);
     const float s = e8m0_value((uint32_t)(k + 127));
     uint32_t d[4];
 #pragma unroll
@@ -223,7 +229,7 @@ __device__ __forceinline__ uint32_t mx4_block(const float (&v)[16], uint2 &codes
     swap32(d[0], d[2]);
     swap32(d[1], d[3]);
     codes = make_uint2(d[0] | (d[2] << 16), d[1] | (d[3] << 16));
-    return (uint32_t)(k + 127);
+    return mx4_scale(top, k);
 }
 __device__ __forceinline__ void store_mx(const float (&v)[16], int fmt, uint8_t *codes, uint8_t *scale, int lh) {
     uint32_t k;

@@ -166,7 +166,8 @@ bsp_status bsp_quantize_mxfp8(const uint16_t *x, int64_t x_rows, int64_t K, int6
  *   flags        0 (nearest, ties to even) or BSP_SR (stochastic)
  * The block exponent is the smallest k with amax <= 6 * 2^k, kept within
  * [-127, 125]; codes = E2M1(x * 2^-k), saturating (which only blocks above
- * 6 * 2^125 reach).  x * 2^-k is taken in f32: exact, except that a value under
+ * 6 * 2^125, infinities among them, reach).  A block with a NaN gets scale code
+ * 255, E8M0's NaN: all its values are NaN.  x * 2^-k is taken in f32: exact, except that a value under
  * 2^-150 of the grid's unit counts as 0.  BSP_SR rounds |x| * 2^-k up to the
  * next E2M1 value iff u < frac * 65536, with frac its exact position between its two grid
  * neighbours and u the 16 bits of Philox4x32-10 (key = seed, counter = i / 8
@@ -220,8 +221,8 @@ bsp_status bsp_quantize_nvfp4_2d(const uint16_t *x, int64_t M, int64_t K, int64_
  *   out      device [M, K] of out_dtype (BSP_DTYPE_F32 or BSP_DTYPE_BF16)
  * NVFP4: y = value(q) * (s * g) in f32 (two rounded products, in that
  * order); MXFP8, MXFP4: y = value(q) * 2^k (exact; a block exponent of 126 or
- * 127, which no quantizer here writes, can exceed f32's range).  bf16 output
- * is the RNE of y.
+ * 127, which no quantizer here writes, can exceed f32's range); MXFP4 blocks
+ * of scale code 255 are NaN.  bf16 output is the RNE of y.
  */
 bsp_status bsp_dequantize(int fmt, const uint8_t *codes, const uint8_t *scales, const float *outer, int64_t M,
                           int64_t K, int64_t rows_per_scale, void *out, int out_dtype, void *stream);
@@ -344,7 +345,7 @@ bsp_status bsp_requant_transpose_sr_batched(const uint8_t *codes, const uint8_t 
  * weights); all modes, no outer scales, WGRAD on the grouped columnwise copies.
  * Products of values times scales are exact and their sums f32: a call's error
  * is f32's rounding of the running sums.  Scale codes are the quantizers': at
- * most 246 (MXFP8) and 252 (MXFP4); with an MXFP8 A, values times scales are
+ * most 246 (MXFP8) and 252 (MXFP4), or 255 for a block of NaN; with an MXFP8 A, values times scales are
  * rounded to multiples of 2^-133.  Calls of at most BSP_FEW_ROWS rows
  * (FPROP, DGRAD) take a form for serving that needs no workspace (size 0, NULL
  * accepted).  Sizes: A's codes and one expert's B below 4 GiB.
@@ -610,7 +611,8 @@ bsp_status bsp_swiglu_checkpoint_backward(const void *dh, int dtype, int64_t R, 
  *   ckpt_codes, ckpt_scales  device u8 [R, 2I], [R, 2I/32], or both NULL (out):
  *            gate and up as rowwise MXFP8, from their f32 values: what
  *            bsp_swiglu_checkpoint_backward and the call below take.  In h and
- *            here a NaN is E4M3's NaN code, infinities are +-448 * 2^119.
+ *            here a NaN is E4M3's NaN code (h in MXFP4: scale code 255, the
+ *            block is NaN), infinities are +-448 * 2^119 (+-6 * 2^125).
  *   workspace  device, >= bsp_moe_gated_workspace_size(fmt, R, I, K, G) bytes,
  *            rewritten by every call; none (NULL) for R <= BSP_FEW_ROWS
  *   tile     0, or 32 / 128 as in bsp_moe_grouped_gemm_blockscaled_tiled

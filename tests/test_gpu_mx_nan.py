@@ -100,3 +100,99 @@ def test_gated_backward_keeps_a_nan_in_its_row(tile):
     keep = torch.arange(ROWS, device=DEV) != NAN_ROW
     for k in got:
         assert torch.equal(got[k][keep], plain[k][keep]), k
+
+
+def special(x):
+    """Some NaN and infinities into bf16 [64, 96]; returns where the NaN are."""
+    nan, inf = float("nan"), float("inf")
+    x[1, 5], x[40, 64], x[40, 65] = nan, nan, inf
+    x[2, 32:64] = -nan
+    x[7, 70], x[63, 95] = inf, -inf
+    return torch.isnan(x)
+
+
+def blocks_with(nan):
+    """Rows [R, K] of truth values -> [R, K / 32]."""
+    return nan.view(nan.shape[0], -1, 32).any(2)
+
+
+@pytest.mark.parametrize("sr", [False, True])
+@pytest.mark.parametrize("form", ["row", "rowcol", "grouped"])
+def test_mxfp4_quantizer(form, sr):
+    """Blocks with a NaN have scale 255 and are NaN when dequantized; all other bytes are those of a tensor without it."""
+    rng = np.random.default_rng(4)
+    x = to_dev_bf16(mx.to_bf16_bits(rng.standard_normal((64, 96)).astype(np.float32)))
+    nan = special(x)
+    kw = dict(colwise=form != "row", sr=sr, seed=9,
+              group_offsets=to_dev(np.array([0, 32, 64], np.int64)) if form == "grouped" else None)
+    q = ops.quantize_mxfp4(x, **kw)
+    plain = ops.quantize_mxfp4(torch.where(nan, torch.zeros_like(x), x), **kw)
+    copies = [("row", blocks_with(nan), x)]
+    if form != "row":
+        copies.append(("colT", blocks_with(nan.t().contiguous()), x.t()))
+    for name, bad, v in copies:
+        codes, scales = q["codes_" + name][:, :bad.shape[1] * 16], q["scales_" + name][:, :bad.shape[1]]
+        assert torch.equal(scales == 255, bad)
+        assert torch.equal(scales[~bad], plain["scales_" + name][:, :bad.shape[1]][~bad])
+        same = (~bad).repeat_interleave(16, 1)
+        assert torch.equal(codes[same], plain["codes_" + name][:, :bad.shape[1] * 16][same])
+        for dtype in (torch.float32, torch.bfloat16):
+            y = ops.dequantize(ops.FMT_MXFP4, codes.contiguous(), scales.contiguous(), out_dtype=dtype)
+            assert torch.equal(torch.isnan(y), bad.repeat_interleave(32, 1))
+            far = torch.isinf(v) & ~bad.repeat_interleave(32, 1)
+            assert (y[far].abs() == 6 * 2.0 ** 125).all() and torch.equal(torch.sign(y[far]), torch.sign(v[far]).to(dtype))
+
+
+def test_every_code_of_a_nan_block_is_nan():
+    codes = torch.arange(256, dtype=torch.uint8, device=DEV).view(16, 16)
+    y = ops.dequantize(ops.FMT_MXFP4, codes, torch.full((16, 1), 255, dtype=torch.uint8, device=DEV))
+    assert torch.isnan(y).all()
+
+
+@pytest.mark.parametrize("a_bits", [4, 8])
+@pytest.mark.parametrize("tile", [32, 128])
+def test_products_of_nan_blocks(tile, a_bits):
+    """A NaN block of the tokens (MXFP4) makes its row NaN, one of the weights its column of that group; K's last stage is
+    not full."""
+    rng = np.random.default_rng(5)
+    K, N = 352, 40
+    ac, as_ = (mx.mxfp4 if a_bits == 4 else mx.mxfp8)(rng.standard_normal((ROWS, K)))
+    bc, bs = mx.mxfp4(rng.standard_normal((2 * N, K)))
+    off = to_dev(np.array([0, 15, ROWS], np.int64))
+    f = ops.FMT_MXFP4 if a_bits == 4 else ops.FMT_MXFP8_MXFP4
+
+    def run():
+        return ops.moe_grouped_gemm_blockscaled(f, ops.GEMM_FPROP, *(to_dev(t) for t in (ac, as_, bc, bs)), off, N, K,
+                                                tile=tile)
+    plain = run()
+    bad = torch.zeros(ROWS, N, dtype=torch.bool, device=DEV)
+    if a_bits == 4:
+        as_[NAN_ROW, 10] = 255
+        bad[NAN_ROW] = True
+    bs[N + 6, 0] = 255
+    bad[15:, 6] = True
+    got = run()
+    assert torch.equal(torch.isnan(got), bad) and torch.equal(got[~bad], plain[~bad])
+
+
+@pytest.mark.parametrize("tile", [32, 128])
+def test_h_in_mxfp4(tile):
+    rng = np.random.default_rng(6)
+    c, s = mx.mxfp8(rng.standard_normal((ROWS, K)))
+    wc, ws = mx.mxfp4(rng.standard_normal((4 * 32, K)))
+    off = to_dev(np.array([0, ROWS], np.int64))
+
+    def run():
+        return ops.moe_gated(ops.FMT_MXFP8_MXFP4, *(to_dev(t) for t in (c, s, wc, ws)), off, 64, K, h_fmt=ops.FMT_MXFP4,
+                             tile=tile)
+    plain = run()
+    c[NAN_ROW, 1] = 0x7F
+    ws[33, 0] = 255                    # gate of column 33: the second block of every row
+    got = run()
+    bad = torch.zeros(ROWS, 2, dtype=torch.bool, device=DEV)
+    bad[NAN_ROW] = True
+    bad[:, 1] = True
+    assert torch.equal(got["scales"] == 255, bad) and torch.equal(got["scales"][~bad], plain["scales"][~bad])
+    same = (~bad).repeat_interleave(16, 1)
+    assert torch.equal(got["codes"][same], plain["codes"][same])
+    assert not (host(plain["scales"]) == 255).any()
