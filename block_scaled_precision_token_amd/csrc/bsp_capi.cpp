@@ -263,8 +263,9 @@ namespace {
 inline bool is_mxfp4(int fmt) { return fmt == BSP_FMT_MXFP4 || fmt == BSP_FMT_MXFP8_MXFP4; }
 
 // Sizes of a grouped product on MX operands: rows and per-lane byte offsets
-// inside an operand (one expert's B) fit 32 bits, grids 2^24 workgroups of 256
-// threads.
+// inside an operand (one expert's B) fit 32 bits, grids fewer than 2^24
+// workgroups of 256 threads: the preparation's is at most M / 64 + G + G (ntn + 1) / 2
+// <= 2 m + 1 + G (ntn + 3) / 2 with m = M / 128, and m + G < grid / (ntn + 1).
 bsp_status mx_shape(int fmt, int mode, int64_t a_rows, int64_t G, int64_t M, int64_t N, int64_t K) {
     const int64_t lim31 = (1ll << 31) - 512, lim32 = 1ll << 32, grid = 1ll << 24;
     if (G < 1 || M <= 0 || N <= 0 || K <= 0 || K % 32 || a_rows <= 0) return BSP_ERR_SHAPE;
@@ -275,7 +276,7 @@ bsp_status mx_shape(int fmt, int mode, int64_t a_rows, int64_t G, int64_t M, int
     if (mode == BSP_GEMM_WGRAD) {
         if (M + N > grid || K / 64 + G + 1 > grid || (M + 127) / 128 * ntn > grid / (G + 8)) return BSP_ERR_SHAPE;
     } else {
-        if (G * ntn > grid || M / 128 + G > grid / (ntn + 1)) return BSP_ERR_SHAPE;
+        if (G * ntn > grid || M / 128 + G >= grid / (ntn + 1)) return BSP_ERR_SHAPE;
     }
     return BSP_OK;
 }

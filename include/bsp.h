@@ -348,7 +348,10 @@ bsp_status bsp_requant_transpose_sr_batched(const uint8_t *codes, const uint8_t 
  * most 246 (MXFP8) and 252 (MXFP4), or 255 for a block of NaN; with an MXFP8 A, values times scales are
  * rounded to multiples of 2^-133.  Calls of at most BSP_FEW_ROWS rows
  * (FPROP, DGRAD) take a form for serving that needs no workspace (size 0, NULL
- * accepted).  Sizes: A's codes and one expert's B below 4 GiB.
+ * accepted).  Sizes (also the gated block's, with N = 2I or I): A's codes and one
+ * expert's B below 4 GiB; with ntn = ceil(N / 128), G ntn <= 2^24 and
+ * M / 128 + G < 2^24 / (ntn + 1); WGRAD: M + N <= 2^24, K / 64 + G < 2^24 and
+ * ceil(M / 128) ntn <= 2^24 / (G + 8).
  *   workspace  device, >= bsp_gemm_workspace_size(fmt, mode, M, N, K, G)
  *              bytes, 16-byte aligned; holds the tile list (WGRAD: the padded
  *              group starts and the experts ordered by token count) and
