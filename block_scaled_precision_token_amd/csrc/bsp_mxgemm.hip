@@ -179,8 +179,8 @@ __device__ __forceinline__ float block_max(const float (&v)[16]) {
     for (int i = 0; i < 16; i++) a = fmaxf(a, fabsf(v[i]));
     return both_max(a);
 }
-// The conversions divide by the block's scale themselves: the same codes as from x * 2^-k for every f32 within the
-// format (checked exhaustively for a dozen exponents).  V_CVT_SCALEF32_PK_FP8_F32 does not saturate: values past
+// The conversions divide by the block's scale themselves: the same codes as from x * 2^-k (tested at every border
+// between two codes and its f32 neighbours, for a dozen exponents).  V_CVT_SCALEF32_PK_FP8_F32 does not saturate: values past
 // 448 * 2^k, as blocks past the largest exponent have, are clamped before it.  A NaN becomes the NaN code on either path
 // (V_MED3_F32 would make it -TOP, in whatever wavefronts clamp).
 __device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d, float scale) {
