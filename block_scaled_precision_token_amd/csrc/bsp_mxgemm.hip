@@ -310,19 +310,18 @@ __device__ __forceinline__ float gated_backward(const Ckpt &k, const v16f &acc, 
     return dw;
 }
 
-// What follows the product of 32 tokens with 64 rows of B, the backward pass apart: acc[j] is block j of them.  Lane l
-// has token row r of C (r < 0: none).  ok: the row's source exists (else it counts as zeros); w: its weight.  col:
-// first column (gated: of the 32 columns of h, acc[0] gate and acc[1] up).  g: group (weight gradient: matrix of C).
-template <int EPI, bool WG>
-__device__ __forceinline__ void epilogue(const MxArgs &p, v16f (&acc)[2], int g, int r, bool ok, float w, int col,
-                                         int lh) {
+// What follows the product of 32 tokens with 64 rows of B in the form for few rows, the backward pass apart: acc[j] is
+// block j of them.  Lane l has token row r of C (r < 0: none).  ok: the row's source exists (else it counts as zeros);
+// w: its weight.  col: first column (gated: of the 32 columns of h, acc[0] gate and acc[1] up).
+template <int EPI>
+__device__ __forceinline__ void epilogue(const MxArgs &p, v16f (&acc)[2], int r, bool ok, float w, int col, int lh) {
     float v[2][16];
 #pragma unroll
     for (int j = 0; j < 2; j++)
 #pragma unroll
         for (int e = 0; e < 16; e++) v[j][e] = ok ? acc[j][e] : 0.0f;
     if constexpr (EPI == EPI_BF16 || EPI == EPI_F32) {
-        const int64_t at = ((WG ? (int64_t)g * p.M : 0) + (r < 0 ? 0 : r)) * p.ldc + col;
+        const int64_t at = (int64_t)(r < 0 ? 0 : r) * p.ldc + col;
 #pragma unroll
         for (int j = 0; j < 2; j++) {
             const int left = r < 0 ? 0 : p.N - (col + 32 * j);   // both lanes of a token exchange in any case
@@ -561,7 +560,7 @@ __global__ __launch_bounds__(512) void k_mx_few(MxArgs p) {
         dw = both_sum(dw);
         if (p.part && r >= 0 && lh == 0) p.part[(int64_t)r * p.parts + col / 64] = dw;
     } else {
-        epilogue<EPI, false>(p, acc, g, r, ok, rw, col, lh);
+        epilogue<EPI>(p, acc, r, ok, rw, col, lh);
     }
 }
 
