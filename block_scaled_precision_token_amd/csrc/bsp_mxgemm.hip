@@ -1468,9 +1468,20 @@ __global__ __launch_bounds__((MxGeo<FT, FN, TB>::NT), 2) void k_mx_tile(MxArgs p
 // ---------------------------------------------------------------------------
 static int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-// Rows of a row tile: 64 for groups of few rows, where the larger tile's products are mostly of rows that are not there
-// (64 / 128: 2048 rows of 128 experts 55 / 66 us; 36864 of 257, 143 each, 1420 / 1300).
-static int tile_rows(bool wgrad, int64_t M, int64_t G) { return wgrad || M / G >= 96 ? 128 : 64; }
+// Rows of a row tile: 64 for groups of few rows, where the larger tile's products are mostly of rows that are not there.
+// us of 64 / 128, by rows of each of 128 groups of 1536 x 2048 (captured calls; the device alone knows how even the
+// groups are):
+//                          80           96         112         128         160         192
+//   MXFP4  product       80 / 75     84 / 83     89 / 85     97 / 86    111 / 96    126 / 100
+//          gated         82 / 82     86 / 93     91 / 95     99 / 96    116 / 109   131 / 114
+//          backward      72 / 71     75 / 87     84 / 91     90 / 92    101 / 99    116 / 105
+//   MXFP8  product      124 / 137   137 / 151   146 / 158   163 / 165   191 / 181   226 / 194
+//   tokens gated        128 / 140   143 / 166   152 / 168   167 / 173   200 / 198   238 / 205
+//          backward      94 / 97    100 / 128   109 / 130   122 / 131   135 / 136   158 / 147
+// and with 143 rows of each of 257 groups of 4096 x 7168, gated, 1542 / 1317 (MXFP4) and 3241 / 3071 (MXFP8 x MXFP4).
+static int tile_rows(int fmt, bool wgrad, bool gated, int64_t M, int64_t G) {
+    return wgrad || M / G >= (fmt == BSP_FMT_MXFP4 && !gated ? 80 : 128) ? 128 : 64;
+}
 
 // Workspace: the d_row_weights parts, then the tiled form's tables and planes, each on a 256-byte boundary.
 struct MxLayout {
@@ -1478,10 +1489,11 @@ struct MxLayout {
     int64_t ntm, ntn, stages;
     int tb;
 };
-static MxLayout layout(int fmt, bool wgrad, int64_t M, int64_t N, int64_t K, int64_t G, int64_t parts,
+// gated: the gated block or its backward pass.
+static MxLayout layout(int fmt, bool wgrad, bool gated, int64_t M, int64_t N, int64_t K, int64_t G, int64_t parts,
                        bool few) {
     MxLayout L = {};
-    L.tb = tile_rows(wgrad, M, G);
+    L.tb = tile_rows(fmt, wgrad, gated, M, G);
     const int64_t bk = fmt == BSP_FMT_MXFP4 ? 256 : 128, sps = bk / 32, nb = L.tb == 128 ? 256 : 128;
     L.tiles = L.a_plane = L.b_plane = L.total = up(M * parts * 4, 256);
     L.ntn = (N + nb - 1) / nb;
@@ -1501,20 +1513,27 @@ static MxLayout layout(int fmt, bool wgrad, int64_t M, int64_t N, int64_t K, int
     }
     return L;
 }
-// Up to 64 rows the form without staging: 32 rows of 128 experts of 1536 x 2048 17.7 us against the tiles' 21.0, 64 rows
-// 28.6 / 29.1, 128 rows 36.7 / 33.2 (MXFP8 x MXFP4, the gated block).
+// Up to 64 rows the form without staging, which needs no workspace and one launch.  us of it / of the tiles, by rows of
+// 128 groups of 1536 x 2048 (captured calls):
+//                          1          16          32          48          64          96         128
+//   MXFP4, gated       12 / 18     16 / 19     20 / 21     22 / 22     26 / 24     30 / 30     35 / 32
+//   MXFP8 x MXFP4      17 / 26     20 / 26     25 / 30     28 / 31     33 / 32     40 / 39     47 / 43
+//   MXFP8              18 / 26     25 / 27     32 / 30     37 / 34     48 / 38     58 / 50     69 / 55
+// (products as the gated block; the backward pass 21 / 24, 25 / 30 and 31 / 32 at 64 rows, 27 / 28, 31 / 36 and 44 / 38
+// at 128).  From about 50 rows, of MXFP8 weights from 24, the tiles are faster where memory for them is at hand; the
+// bound is one for all, so that a serving loop's calls need no workspace.
 static bool few_rows(int mode, int64_t M, int tile) {
     return mode != BSP_GEMM_WGRAD && (tile == 32 || (tile == 0 && M <= BSP_FEW_ROWS));
 }
 
 int64_t mx_gemm_workspace_bytes(int fmt, int mode, int64_t M, int64_t N, int64_t K, int64_t G, int tile) {
-    return layout(fmt, mode == BSP_GEMM_WGRAD, M, N, K, G, 0, few_rows(mode, M, tile)).total;
+    return layout(fmt, mode == BSP_GEMM_WGRAD, false, M, N, K, G, 0, few_rows(mode, M, tile)).total;
 }
 int64_t mx_gated_workspace_bytes(int fmt, int64_t R, int64_t I, int64_t K, int64_t G, int tile) {
-    return layout(fmt, false, R, 2 * I, K, G, 0, few_rows(BSP_GEMM_FPROP, R, tile)).total;
+    return layout(fmt, false, true, R, 2 * I, K, G, 0, few_rows(BSP_GEMM_FPROP, R, tile)).total;
 }
 int64_t mx_gated_bwd_workspace_bytes(int fmt, int64_t R, int64_t I, int64_t K, int64_t G, bool sums, int tile) {
-    return layout(fmt, false, R, I, K, G, sums ? (I + 63) / 64 : 0, few_rows(BSP_GEMM_FPROP, R, tile)).total;
+    return layout(fmt, false, true, R, I, K, G, sums ? (I + 63) / 64 : 0, few_rows(BSP_GEMM_FPROP, R, tile)).total;
 }
 
 template <int FT, int FN, int EPI>
@@ -1581,7 +1600,7 @@ hipError_t launch_mx_gemm(int fmt, int mode, const uint8_t *a_codes, const uint8
     MxArgs p = operands(a_codes, a_scales, gather, a_rows, off, G, M, N, K, b_codes, b_scales);
     p.c = c; p.ldc = ldc;
     const bool wgrad = mode == BSP_GEMM_WGRAD, few = few_rows(mode, M, tile);
-    const MxLayout L = layout(fmt, wgrad, M, N, K, G, 0, few);
+    const MxLayout L = layout(fmt, wgrad, false, M, N, K, G, 0, few);
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
     if (c_dtype == BSP_DTYPE_BF16) launch_gemm_epi<EPI_BF16>(fmt, wgrad, p, few, L, ws, s);
     else launch_gemm_epi<EPI_F32>(fmt, wgrad, p, few, L, ws, s);
@@ -1605,7 +1624,7 @@ hipError_t launch_moe_gated(int fmt, const uint8_t *a_codes, const uint8_t *a_sc
     p.row_weights = row_weights; p.h = h; p.h_fmt = h_fmt; p.h_codes = h_codes; p.h_scales = h_scales;
     p.ckpt_codes = ckpt_codes; p.ckpt_scales = ckpt_scales; p.I = (int32_t)I;
     const bool few = few_rows(BSP_GEMM_FPROP, R, tile);
-    return launch_gated_epi<EPI_GATED>(fmt, p, few, layout(fmt, false, R, 2 * I, K, G, 0, few),
+    return launch_gated_epi<EPI_GATED>(fmt, p, few, layout(fmt, false, true, R, 2 * I, K, G, 0, few),
                                        reinterpret_cast<uint8_t *>(workspace), s);
 }
 
@@ -1620,7 +1639,7 @@ hipError_t launch_moe_gated_backward(int fmt, const uint8_t *dy_codes, const uin
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
     const int64_t parts = d_row_weights ? (I + 63) / 64 : 0;
     const bool few = few_rows(BSP_GEMM_FPROP, R, tile);
-    const MxLayout L = layout(fmt, false, R, I, K, G, parts, few);
+    const MxLayout L = layout(fmt, false, true, R, I, K, G, parts, few);
     p.parts = (int32_t)parts;
     p.part = d_row_weights ? reinterpret_cast<float *>(ws) : nullptr;
     const hipError_t e = launch_gated_epi<EPI_GATED_BWD>(fmt, p, few, L, ws, s);

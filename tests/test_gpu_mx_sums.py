@@ -43,8 +43,8 @@ def problem(fmt, sizes, N, K, seed):
     return f, [to_dev(t) for t in (ac, as_, bc, bs, off)], ref, refabs
 
 
-# few rows; tiles of 64 rows; tiles of 128
-FORMS = [(32, [5, 0, 40]), (128, [5, 0, 40]), (128, [130, 97])]
+# few rows; tiles of 64 rows; of 128 for MXFP4 products, else 64; of 128
+FORMS = [(32, [5, 0, 40]), (128, [5, 0, 40]), (128, [130, 97]), (128, [300, 97])]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
