@@ -196,3 +196,36 @@ def test_h_in_mxfp4(tile):
     same = (~bad).repeat_interleave(16, 1)
     assert torch.equal(got["codes"][same], plain["codes"][same])
     assert not (host(plain["scales"]) == 255).any()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "a8w4", "mxfp8"])
+@pytest.mark.parametrize("rows", [ROWS, 400])
+def test_rows_without_a_source_are_zeros_beside_nan(rows, fmt):
+    """Indices outside x, where the tokens of its first row, which such rows may load, are NaN."""
+    f, ab, bb = {"mxfp4": (ops.FMT_MXFP4, 4, 4), "a8w4": (ops.FMT_MXFP8_MXFP4, 8, 4), "mxfp8": (ops.FMT_MXFP8, 8, 8)}[fmt]
+    rng = np.random.default_rng(7)
+    quantize = {4: mx.mxfp4, 8: mx.mxfp8}
+    c, s = quantize[ab](rng.standard_normal((6, K)))
+    if ab == 4:
+        s[0] = 255
+    else:
+        c[0] = 0x7F
+    w13, w2 = (quantize[bb](rng.standard_normal((n, K))) for n in (2 * I, I))
+    ck = mx.mxfp8(rng.standard_normal((rows, 2 * I)))
+    gather = rng.integers(1, 6, rows).astype(np.int32)
+    gather[::3] = rng.choice([-1, 6, 2 ** 31 - 1, -2 ** 31], len(gather[::3]))
+    none = torch.from_numpy(gather < 0).to(DEV) | torch.from_numpy(gather > 5).to(DEV)
+    off, idx, rw = to_dev(np.array([0, rows], np.int64)), to_dev(gather), torch.rand(rows, device=DEV)
+    a = [to_dev(t) for t in (c, s)]
+    out = ops.moe_gated(f, *a, *(to_dev(t) for t in w13), off, I, K, a_gather=idx, row_weights=rw, checkpoint=True,
+                        return_h=True)
+    assert not torch.isnan(out["h"]).any() and (out["h"][none] == 0).all() and (out["h"][~none] != 0).any()
+    for k in ("codes", "ckpt_codes"):
+        assert (out[k][none] & 127 == 0).all() and (out[k] & 127 != 127).all()
+    back = ops.moe_gated_backward(f, *a, *(to_dev(t) for t in w2), off, I, K, *(to_dev(t) for t in ck), a_gather=idx,
+                                  row_weights=rw)
+    assert (back["dh13"][none] == 0).all() and (back["d_row_weights"][none] == 0).all()
+    assert torch.isfinite(back["dh13"].float()).all() and torch.isfinite(back["d_row_weights"]).all()
+    if fmt != "mxfp8":
+        y = ops.moe_grouped_gemm_blockscaled(f, ops.GEMM_FPROP, *a, *(to_dev(t) for t in w13), off, 2 * I, K, a_gather=idx)
+        assert (y[none] == 0).all() and torch.isfinite(y).all()
