@@ -6,8 +6,9 @@
 //   code = E2M1(x * 2^-k): x * 2^-k is exact in f32 (0 far below the grid), so each value is rounded once
 //   a block with a NaN: scale 255, with which the conversions and the matrix instructions give NaN for any code
 //
-// HBM bounds: 2 bytes in and 17/32 bytes out per value and copy.  8192 x 2048 in
-// both copies takes 15 us (51 MB, 3.4 TB/s), 65536 x 1536 by groups and rounded
+// HBM bounds: 2 bytes in and 17/32 bytes out per value and copy.  8192 x 2048
+// takes 10 us rowwise (42 MB, 4.2 TB/s) and 15 in both copies (51 MB, 3.4 TB/s),
+// 65536 x 1536 by groups and rounded
 // stochastically 147 us (302 MB, 2.1 TB/s): there the generator's vector
 // instructions bound it, as they do every stochastic rounding here.
 #include "bsp_moe.hpp"

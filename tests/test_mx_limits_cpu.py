@@ -5,7 +5,8 @@ import pytest
 from block_scaled_precision_token_amd import ops
 from tests.test_mx_args_cpu import P, SHAPE, back, gated, gemm
 
-# groups of 94 rows take 64-row tiles: M / 64 + G workgroups for these and G for 128 columns
+# groups of 94 rows, in 64-row tiles (the gated block, MXFP8 tokens): M / 64 + G workgroups for these and G for 128
+# columns; MXFP4 products, in 128-row tiles, have the same bound
 G = 4823450
 M = 128 * ((1 << 23) - G)
 
